@@ -402,6 +402,169 @@ QCAST_API int qcast_per_channel_sf(const void* x, int64_t rows, int64_t cols, in
 QCAST_API int qcast_cast_back(const void* q, const float* sf, int64_t rows, int64_t cols, int fmt,
                               int group, int out_dtype, void* out, void* stream);
 
+/*
+ * SwiGLU forward fused with the per-token cast and with an 8-bit checkpoint
+ * of its input, for a backward pass that reads the checkpoint instead of h
+ * (qcast_swiglu_backward_checkpoint): one read of h.
+ *   h, row_weight, fmt, group, clamp_min, sf_flags, swiglu_clamp, q, sf: as
+ *             qcast_swiglu_per_token_ex (nothing is counted). v comes from h
+ *             itself, not from the checkpoint.
+ *   ckpt_fmt  QCAST_FMT_E4M3 or QCAST_FMT_E5M2.
+ *   ckpt      [rows, 2*cols] codes and ckpt_sf [rows, 2*cols/group] fp32 of
+ *             h, bit for bit as qcast_per_token(h, ckpt_fmt, group) with the
+ *             default floor writes them.
+ */
+QCAST_API int qcast_swiglu_checkpoint(const void* h, int64_t rows, int64_t cols,
+                                      const float* row_weight, int fmt, int group,
+                                      float clamp_min, int sf_flags, float swiglu_clamp, void* q,
+                                      void* sf, int ckpt_fmt, void* ckpt, float* ckpt_sf,
+                                      void* stream);
+
+/*
+ * SwiGLU backward from the 8-bit checkpoint of its input, with the operands
+ * of every product that follows it. With h = decode(ckpt) * ckpt_sf (fp32)
+ * and the derivative of qcast_swiglu_backward_per_token:
+ *   q      [rows, 2*cols] codes of [dg | du] and sf, as that entry point
+ *          writes them in group 128 with sf_flags: for dX.
+ *   dhT    the codes of [dg | du] transposed, dhT_sf their scales: for dW of
+ *          the gate and up projections. vT, vT_sf: the same of v = silu(g) *
+ *          u * row_weight, formed again from the checkpoint: for dW of the
+ *          down projection. NULL (with NULL scales) leaves either out.
+ *          The transposed rows hold rows_T = ceil(rows/128)*128 codes; the
+ *          codes past `rows` are zero. Otherwise as qcast_per_channel_T_sf
+ *          writes a [rows_T, 2*cols] or [rows_T, cols] input with sf_flags
+ *          (packed needs (rows_T/128) % 4 == 0, and 4 | cols/128).
+ *   dw     [rows] fp32 or NULL: the gradient of row_weight,
+ *          sum_j dv[r][j] * silu(g) * u (also when row_weight is NULL).
+ *   ckpt   [rows, 2*cols] codes in ckpt_fmt (E4M3 or E5M2), ckpt_sf [rows,
+ *          2*cols/128] fp32; dv [rows, cols] bf16; row_weight [rows] or NULL.
+ *   fmt    QCAST_FMT_E4M3 or QCAST_FMT_E5M2; group must be 128;
+ *          cols % 128 == 0.
+ *   ws     NULL, or rows * (cols/128) * 4 bytes of device memory (16-byte
+ *          aligned; no particular contents) that no other call uses at the
+ *          same time. Needed when dw is given and cols > 128.
+ *   Limits: 256 * cols < 2^31, 128 * rows_T < 2^31,
+ *   ceil(rows/128) * (cols/128) < 2^31 - 16.
+ */
+QCAST_API int qcast_swiglu_backward_checkpoint(
+    const void* ckpt, const float* ckpt_sf, const void* dv, int64_t rows, int64_t cols,
+    const float* row_weight, int ckpt_fmt, int fmt, int group, float clamp_min, int sf_flags,
+    float swiglu_clamp, void* q, void* sf, void* dhT, void* dhT_sf, void* vT, void* vT_sf,
+    float* dw, void* ws, void* stream);
+
+/*
+ * Stored per-token codes cast again along the tokens and written transposed:
+ * the operand of a weight gradient (dW = X^T dY) from the X that the forward
+ * pass kept in 8 bits.
+ *   q_in   [rows, cols] codes in in_fmt (E4M3 or E5M2), sf_in [rows,
+ *          cols/in_group] fp32, as qcast_per_token writes them; in_group 32,
+ *          64 or 128, cols % in_group == 0 and cols % 16 == 0.
+ *   x      = decode(q_in) * sf_in (fp32, not rounded further).
+ *   qT     one code row of rows_T = ceil(rows/128)*128 codes per channel, in
+ *          fmt (E4M3 or E5M2); codes past `rows` are zero. sf its scales:
+ *          both as qcast_per_channel_T_sf writes the [rows_T, cols] input x
+ *          with sf_flags (packed needs (rows_T/128) % 4 == 0).
+ *   group  must be 128.
+ *   Limits: 128 * cols < 2^31, 128 * rows_T < 2^31,
+ *   ceil(rows/128) * ceil(cols/128) < 2^31 - 16.
+ */
+QCAST_API int qcast_recast_per_channel_T(const void* q_in, const float* sf_in, int64_t rows,
+                                         int64_t cols, int in_fmt, int in_group, int fmt,
+                                         int group, float clamp_min, int sf_flags, void* qT,
+                                         void* sf, void* stream);
+
+/* What the gate of the norm entry points is broadcast along. */
+typedef enum {
+  QCAST_GATE_NONE = 0,
+  QCAST_GATE_CHANNEL = 1, /* [cols] bf16 */
+  QCAST_GATE_TOKEN = 2,   /* [rows] fp32 */
+  QCAST_GATE_FULL = 3     /* [rows, cols] bf16 */
+} qcast_gate_kind;
+
+/* Longest row of the norm entry points. */
+#define QCAST_NORM_MAX_COLS 32768
+
+/*
+ * The norm after a block, its gate and the scaled residual, the norm before
+ * the next block and the per-token cast of that block's input, in one pass
+ * over the row:
+ *   a  = y / sqrt(mean(y^2) + eps)        (a = y when w_post is NULL)
+ *   h' = residual_scale * h + a * (w_post + weight_offset) * gate
+ *   x  = h' / sqrt(mean(h'^2) + eps) * (w_pre + weight_offset)
+ * in fp32; x and its norm come from h' before it is rounded to the bf16 that
+ * h_out holds.
+ *   y        [rows, cols] bf16, the block's output, or NULL before the first
+ *            block: then h' = h, and w_post, gate, h_out, rstd_post and
+ *            y_ckpt must be NULL (gate_kind QCAST_GATE_NONE) and
+ *            residual_scale 1.
+ *   h        [rows, cols] bf16, the residual stream. h_out [rows, cols] bf16.
+ *   w_post, w_pre  [cols] bf16; weight_offset is added to both (0, or 1 for
+ *            weights stored around zero). w_post may be NULL: no post-norm.
+ *   gate     as gate_kind says, or NULL with QCAST_GATE_NONE.
+ *   q, sf    the cast of x: fmt, group, clamp_min, sf_flags as
+ *            qcast_per_token_sf. q and sf may both be NULL when x_out is given.
+ *   x_out    [rows, cols] bf16 (x rounded), or NULL.
+ *   rstd_post, rstd_pre  [rows] fp32, the two factors 1 / sqrt(...), or NULL;
+ *            rstd_post must be NULL without w_post.
+ *   y_ckpt, y_ckpt_sf, h_ckpt, h_ckpt_sf  8-bit checkpoints for the backward
+ *            pass, [rows, cols] codes in ckpt_fmt (E4M3 or E5M2) and [rows,
+ *            cols/128] scales: the per-token casts (group 128, default floor)
+ *            of y and of the fp32 h'. Each pair may be NULL; with neither,
+ *            ckpt_fmt is ignored. They need cols % 128 == 0.
+ *   eps      finite and >= 0; residual_scale and weight_offset finite.
+ *   group 32, 64 or 128; cols % group == 0; cols <= QCAST_NORM_MAX_COLS;
+ *   rows < 2^31. Every bf16 tensor and code output is 16-byte aligned.
+ */
+QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t cols,
+                                   const void* w_post, const void* w_pre, const void* gate,
+                                   int gate_kind, float residual_scale, float weight_offset,
+                                   float eps, int fmt, int group, float clamp_min, int sf_flags,
+                                   void* h_out, void* q, void* sf, void* x_out,
+                                   float* rstd_post, float* rstd_pre, int ckpt_fmt, void* y_ckpt,
+                                   float* y_ckpt_sf, void* h_ckpt, float* h_ckpt_sf,
+                                   void* stream);
+
+/* Rows of partial sums of qcast_norm_backward_per_token's workspace. */
+#define QCAST_NORM_WS_ROWS 512
+
+/*
+ * Gradient of qcast_norm_per_token, fused with the per-token cast of the
+ * block's output gradient. With dx the gradient of x, dh_in that of h' along
+ * the residual stream, xh = h' * rstd_pre, a = y * rstd_post (a = y without
+ * w_post), wq = w_pre + weight_offset, wp = w_post + weight_offset (1 without):
+ *   dH = dh_in + rstd_pre * (dx * wq - xh * mean(dx * wq * xh))
+ *   dh = residual_scale * dH
+ *   dz = dH * gate
+ *   dy = rstd_post * (dz * wp - a * mean(dz * wp * a))      (dz without w_post)
+ *   dw_pre = sum_rows dx * xh,  dw_post = sum_rows dz * a
+ *   dgate  = dH * a * wp, summed over what the gate is broadcast along
+ * in fp32, the column sums too (in an order fixed by the sizes).
+ *   dx       [rows, cols] bf16; dh_in [rows, cols] bf16 or NULL (zero).
+ *   saved_fmt 0: saved_h and saved_y are h_out and y, bf16, and the scales
+ *            are NULL. QCAST_FMT_E4M3 / QCAST_FMT_E5M2: they are the checkpoints
+ *            h_ckpt and y_ckpt with scales [rows, cols/128]; cols % 128 == 0.
+ *   saved_y  NULL where the forward call had no y: then w_post, gate,
+ *            rstd_post, q, sf, dy_out, dw_post and dgate must be NULL.
+ *   rstd_post is given exactly when w_post is.
+ *   dh_out   [rows, cols] bf16.
+ *   q, sf    the cast of dy: fmt, group, clamp_min, sf_flags as
+ *            qcast_per_token_sf; dy_out [rows, cols] bf16. With saved_y at
+ *            least one of q (with sf) and dy_out is given.
+ *   dw_pre, dw_post  [cols] fp32; dgate [cols] fp32, [rows] fp32 or [rows,
+ *            cols] bf16 by gate_kind. Each may be NULL; all are overwritten.
+ *   ws       min(rows, QCAST_NORM_WS_ROWS) * 3 * cols * 4 bytes of device
+ *            memory (16-byte aligned; no particular contents) that no other
+ *            call uses at the same time; may be NULL when rows <= 1.
+ *   Everything else as qcast_norm_per_token.
+ */
+QCAST_API int qcast_norm_backward_per_token(
+    const void* dx, const void* dh_in, int64_t rows, int64_t cols, int saved_fmt,
+    const void* saved_h, const float* saved_h_sf, const void* saved_y, const float* saved_y_sf,
+    const float* rstd_post, const float* rstd_pre, const void* w_post, const void* w_pre,
+    const void* gate, int gate_kind, float residual_scale, float weight_offset, int fmt,
+    int group, float clamp_min, int sf_flags, void* dh_out, void* q, void* sf, void* dy_out,
+    float* dw_post, float* dw_pre, void* dgate, void* ws, void* stream);
+
 /* Human-readable name of a status code (static string). */
 QCAST_API const char* qcast_status_str(int status);
 

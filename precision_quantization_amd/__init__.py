@@ -18,10 +18,14 @@ per-block and per-channel casts, tokens for the transposed per-channel ones.
 mirrors the call shown in the quick start of the page
 "DeepSeek开源TileKernels：用Python写的GPU算子逼近硬件性能上限".
 """
+from collections import namedtuple
+from contextlib import nullcontext
+
 import torch
 
-from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E5M2, FMT_E5M6, OUT_BF16, OUT_F32, SF_COL_MAJOR,
-                   SF_PACKED_UE8M0, SF_ROUND_POW2, QcastError, check, fmt_id, load)
+from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E5M2, FMT_E5M6, GATE_CHANNEL, GATE_FULL, GATE_NONE,
+                   GATE_TOKEN, NORM_WS_ROWS, OUT_BF16, OUT_F32, SF_COL_MAJOR, SF_PACKED_UE8M0,
+                   SF_ROUND_POW2, QcastError, check, fmt_id, load)
 
 __all__ = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per_block",
            "qcast_per_channel_T", "qcast_cast_back", "qcast_per_token_sf",
@@ -29,7 +33,10 @@ __all__ = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_swiglu_backward_per_token", "qcast_swiglu_per_channel_T", "qcast_per_channel",
            "qcast_swiglu_per_token_noalloc", "qcast_per_block_sf", "qcast_per_channel_sf",
            "qcast_per_channel_T_sf", "qcast_swiglu_per_channel_T_sf",
-           "qcast_swiglu_backward_per_token_sf", "sf_layout_shape", "SF_ROUND_POW2", "SF_COL_MAJOR",
+           "qcast_swiglu_backward_per_token_sf", "qcast_swiglu_checkpoint",
+           "qcast_swiglu_backward_checkpoint", "qcast_recast_per_channel_T",
+           "qcast_norm_per_token", "qcast_norm_backward_per_token", "SwigluGrad", "NormOut",
+           "NormGrad", "sf_layout_shape", "SF_ROUND_POW2", "SF_COL_MAJOR",
            "SF_PACKED_UE8M0", "qcast_abi_version", "qcast_set_num_cus", "qcast_bench_copy",
            "qcast_bench_check_scale", "qcast_bench_time_next",
            "qcast_bench_per_channel_T_traffic",
@@ -523,6 +530,294 @@ def qcast_cast_back(q, sf, fmt="e4m3", group=128, out_dtype=torch.bfloat16, out=
         check(load().qcast_cast_back(q.data_ptr(), sf.data_ptr(), rows, cols, f, group, od,
                                      out.data_ptr(), _stream(q.device, stream)), "qcast_cast_back")
     return out
+
+
+# ---- around the products of a training step: checkpoints and norms ----------
+
+SwigluGrad = namedtuple("SwigluGrad", "dh dh_sf dh_t dh_t_sf v_t v_t_sf dw")
+NormOut = namedtuple("NormOut", "h out out_sf x rstd_post rstd_pre y_ckpt y_ckpt_sf h_ckpt "
+                                "h_ckpt_sf")
+NormGrad = namedtuple("NormGrad", "dh out out_sf dy dw_post dw_pre dgate")
+_HERE = nullcontext()
+
+
+def _placed(device, stream):
+    """The handle of the stream a call runs on and the context in which it
+    allocates: outputs and workspaces come from that stream's pool, so memory
+    still in use on the current stream is never handed to another one."""
+    current = torch.cuda.current_stream(device)
+    handle = current.cuda_stream if stream is None else _stream(device, stream)
+    if handle != current.cuda_stream:
+        s = torch.cuda.default_stream(device) if handle == 0 else \
+            torch.cuda.ExternalStream(handle, device=device)
+        return handle, torch.cuda.stream(s)
+    if device.index != torch.cuda.current_device():
+        return handle, torch.cuda.device(device)
+    return handle, _HERE
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _codes(q, name):
+    """Stored 8-bit codes ``[rows, cols]`` and their format, from the dtype."""
+    f = {torch.float8_e4m3fn: FMT_E4M3, torch.float8_e5m2: FMT_E5M2}.get(
+        getattr(q, "dtype", None))
+    if f is None or not q.is_cuda:
+        raise QcastError(4, f"{name} must be a float8_e4m3fn or float8_e5m2 CUDA (HIP) tensor")
+    if q.dim() != 2 or not q.is_contiguous():
+        raise QcastError(2, f"{name} must be a contiguous 2-D tensor")
+    return f
+
+
+def _like(t, shape, dtype, device, name):
+    """An input that has to have this shape and type; returns its pointer."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+            t.device != device or not t.is_contiguous():
+        raise QcastError(2, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+    return t.data_ptr()
+
+
+def qcast_swiglu_checkpoint(h, row_weight=None, fmt="e4m3", group=128, clamp_min=0.0, sf_flags=0,
+                            swiglu_clamp=0.0, ckpt_fmt="e4m3", out=None, out_sf=None, ckpt=None,
+                            ckpt_sf=None, stream=None):
+    """SwiGLU of ``h [rows, 2N]`` cast per token, and the 8-bit per-token cast
+    of ``h`` itself for qcast_swiglu_backward_checkpoint: ``(out [rows, N],
+    out_sf, ckpt [rows, 2N], ckpt_sf [rows, 2N/group])``."""
+    f, cf = fmt_id(fmt), fmt_id(ckpt_fmt)
+    h, rows, cols = _gate_up(h)
+    if cf not in (FMT_E4M3, FMT_E5M2):
+        raise QcastError(4, "ckpt_fmt must be an 8-bit format (e4m3 or e5m2)")
+    dev = h.device
+    wptr = _row_weight(row_weight, rows, dev)
+    g = group if group > 0 else 1
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _out(out, code_shape(f, rows, cols), _code_dtype(f), dev, "out")
+        shape, dt = sf_layout_shape(rows, cols, g, sf_flags)
+        out_sf = _out(out_sf, shape, dt, dev, "out_sf")
+        ckpt = _out(ckpt, (rows, 2 * cols), _code_dtype(cf), dev, "ckpt")
+        ckpt_sf = _out(ckpt_sf, (rows, 2 * cols // g), torch.float32, dev, "ckpt_sf")
+        check(load().qcast_swiglu_checkpoint(
+            h.data_ptr(), rows, cols, wptr, f, group, clamp_min, sf_flags, swiglu_clamp,
+            out.data_ptr(), out_sf.data_ptr(), cf, ckpt.data_ptr(), ckpt_sf.data_ptr(), sh),
+            "qcast_swiglu_checkpoint")
+    return out, out_sf, ckpt, ckpt_sf
+
+
+def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4m3", group=128,
+                                     clamp_min=0.0, sf_flags=0, swiglu_clamp=0.0,
+                                     transposed=True, weight_grad=True, stream=None):
+    """SwiGLU backward from the 8-bit checkpoint ``ckpt [rows, 2N]`` (its format
+    is its dtype) with scales ``ckpt_sf [rows, 2N/128]``: a ``SwigluGrad`` of
+    ``dh [rows, 2N]`` codes of [dgate | dup] and ``dh_sf``; with ``transposed``
+    ``dh_t [2N, rows_T]``, ``v_t [N, rows_T]`` and their scales, the operands of
+    the weight gradients, rows_T = rows up to a multiple of 128 and the codes
+    behind the last row zero; with ``weight_grad`` ``dw [rows]``, the gradient
+    of ``row_weight``. What is not asked for is None."""
+    f = fmt_id(fmt)
+    cf = _codes(ckpt, "ckpt")
+    rows, two_n = ckpt.shape
+    if two_n % 2:
+        raise QcastError(2, f"ckpt must have an even number of columns (gate | up), got {two_n}")
+    if f not in (FMT_E4M3, FMT_E5M2):
+        raise QcastError(4, "fmt must be an 8-bit format (e4m3 or e5m2)")
+    cols = two_n // 2
+    dev = ckpt.device
+    sfptr = _like(ckpt_sf, (rows, two_n // 128), torch.float32, dev, "ckpt_sf")
+    dvptr = _like(dv, (rows, cols), torch.bfloat16, dev, "dv")
+    wptr = _row_weight(row_weight, rows, dev)
+    rows_t = (rows + 127) // 128 * 128
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        dt8 = _code_dtype(f)
+        dh = torch.empty((rows, two_n), dtype=dt8, device=dev)
+        shape, dt = sf_layout_shape(rows, two_n, 128, sf_flags)
+        dh_sf = torch.empty(shape, dtype=dt, device=dev)
+        dh_t = dh_t_sf = v_t = v_t_sf = dw = ws = None
+        if transposed:
+            dh_t = torch.empty((two_n, rows_t), dtype=dt8, device=dev)
+            v_t = torch.empty((cols, rows_t), dtype=dt8, device=dev)
+            dh_t_sf = torch.empty(sf_layout_shape(two_n, rows_t, 128, sf_flags)[0], dtype=dt,
+                                  device=dev)
+            v_t_sf = torch.empty(sf_layout_shape(cols, rows_t, 128, sf_flags)[0], dtype=dt,
+                                 device=dev)
+        if weight_grad:
+            dw = torch.empty(rows, dtype=torch.float32, device=dev)
+            if cols > 128:
+                ws = torch.empty(rows * (cols // 128), dtype=torch.float32, device=dev)
+        check(load().qcast_swiglu_backward_checkpoint(
+            ckpt.data_ptr(), sfptr, dvptr, rows, cols, wptr, cf, f, group, clamp_min, sf_flags,
+            swiglu_clamp, dh.data_ptr(), dh_sf.data_ptr(), _ptr(dh_t), _ptr(dh_t_sf), _ptr(v_t),
+            _ptr(v_t_sf), _ptr(dw), _ptr(ws), sh), "qcast_swiglu_backward_checkpoint")
+    return SwigluGrad(dh, dh_sf, dh_t, dh_t_sf, v_t, v_t_sf, dw)
+
+
+def qcast_recast_per_channel_T(q, sf, fmt="e4m3", group=128, clamp_min=0.0, sf_flags=0, out=None,
+                               out_sf=None, stream=None):
+    """Stored per-token codes ``q [rows, cols]`` (their format is their dtype)
+    with scales ``sf [rows, cols/g]`` (g = 32, 64 or 128) cast again along the
+    tokens and transposed: ``out [cols, rows_T]``, ``out_sf`` in the layouts of
+    ``sf_layout_shape(cols, rows_T, 128, sf_flags)``, rows_T = rows up to a
+    multiple of 128 and the codes behind the last row zero."""
+    f = fmt_id(fmt)
+    cf = _codes(q, "q")
+    rows, cols = q.shape
+    if f not in (FMT_E4M3, FMT_E5M2):
+        raise QcastError(4, "fmt must be an 8-bit format (e4m3 or e5m2)")
+    dev = q.device
+    if not isinstance(sf, torch.Tensor) or sf.dim() != 2 or sf.shape[0] != rows or \
+            (sf.shape[1] == 0) != (cols == 0) or (cols and cols % sf.shape[1]):
+        raise QcastError(2, "sf must be a [rows, cols/g] tensor")
+    in_group = cols // sf.shape[1] if cols else 128
+    sfptr = _like(sf, sf.shape, torch.float32, dev, "sf")
+    rows_t = (rows + 127) // 128 * 128
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _out(out, (cols, rows_t), _code_dtype(f), dev, "out")
+        shape, dt = sf_layout_shape(cols, rows_t, 128, sf_flags)
+        out_sf = _out(out_sf, shape, dt, dev, "out_sf")
+        check(load().qcast_recast_per_channel_T(
+            q.data_ptr(), sfptr, rows, cols, cf, in_group, f, group, clamp_min, sf_flags,
+            out.data_ptr(), out_sf.data_ptr(), sh), "qcast_recast_per_channel_T")
+    return out, out_sf
+
+
+def _gate_arg(gate, rows, cols, device):
+    """(kind, pointer) of a gate: [cols] bf16, [rows] fp32 or [rows, cols] bf16."""
+    if gate is None:
+        return GATE_NONE, None
+    if isinstance(gate, torch.Tensor) and gate.dtype == torch.float32:
+        return GATE_TOKEN, _like(gate, (rows,), torch.float32, device, "gate")
+    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+        return GATE_CHANNEL, _like(gate, (cols,), torch.bfloat16, device, "gate")
+    return GATE_FULL, _like(gate, (rows, cols), torch.bfloat16, device, "gate")
+
+
+def qcast_norm_per_token(h, w_pre, y=None, w_post=None, gate=None, residual_scale=1.0,
+                         weight_offset=0.0, eps=1e-6, fmt="e4m3", group=128, clamp_min=0.0,
+                         sf_flags=0, ckpt_fmt=None, want_x=False, want_codes=True, stream=None):
+    """Norm after a block (``y``, weight ``w_post``), its ``gate`` and the scaled
+    residual ``h``, the norm before the next block (``w_pre``) and the per-token
+    cast of that block's input (include/qcast.h). ``gate``: bf16 ``[cols]``,
+    fp32 ``[rows]`` or bf16 ``[rows, cols]``.
+
+    Returns a ``NormOut``: ``h`` the new residual stream (the given one without
+    ``y``), ``out``/``out_sf`` the cast (with ``want_codes``), ``x`` the bf16
+    input (with ``want_x``), ``rstd_post``/``rstd_pre``, and with ``ckpt_fmt``
+    ('e4m3' or 'e5m2') the 8-bit checkpoints of ``y`` and of the new residual
+    stream for qcast_norm_backward_per_token."""
+    f = fmt_id(fmt)
+    h = _bf16_input(h, "h")
+    rows, cols = h.shape
+    dev = h.device
+    bf16, f32 = torch.bfloat16, torch.float32
+    wqptr = _like(w_pre, (cols,), bf16, dev, "w_pre")
+    yptr = None if y is None else _like(y, (rows, cols), bf16, dev, "y")
+    wpptr = None if w_post is None else _like(w_post, (cols,), bf16, dev, "w_post")
+    kind, gptr = _gate_arg(gate, rows, cols, dev)
+    if y is None and (w_post is not None or gate is not None):
+        raise QcastError(1, "w_post and gate need y")
+    cf = 0 if ckpt_fmt is None else fmt_id(ckpt_fmt)
+    if cf not in (0, FMT_E4M3, FMT_E5M2):
+        raise QcastError(4, "ckpt_fmt must be an 8-bit format (e4m3 or e5m2)")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        h_out = h if y is None else torch.empty((rows, cols), dtype=bf16, device=dev)
+        out = out_sf = x = r1 = yc = yc_sf = hc = hc_sf = None
+        if want_codes:
+            out = torch.empty(code_shape(f, rows, cols), dtype=_code_dtype(f), device=dev)
+            shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
+            out_sf = torch.empty(shape, dtype=dt, device=dev)
+        if want_x:
+            x = torch.empty((rows, cols), dtype=bf16, device=dev)
+        r2 = torch.empty(rows, dtype=f32, device=dev)
+        if w_post is not None:
+            r1 = torch.empty(rows, dtype=f32, device=dev)
+        if cf:
+            hc = torch.empty((rows, cols), dtype=_code_dtype(cf), device=dev)
+            hc_sf = torch.empty((rows, cols // 128), dtype=f32, device=dev)
+            if y is not None:
+                yc, yc_sf = torch.empty_like(hc), torch.empty_like(hc_sf)
+        check(load().qcast_norm_per_token(
+            yptr, h.data_ptr(), rows, cols, wpptr, wqptr, gptr, kind, residual_scale,
+            weight_offset, eps, f, group, clamp_min, sf_flags,
+            None if y is None else h_out.data_ptr(), _ptr(out), _ptr(out_sf), _ptr(x), _ptr(r1),
+            r2.data_ptr(), cf, _ptr(yc), _ptr(yc_sf), _ptr(hc), _ptr(hc_sf), sh),
+            "qcast_norm_per_token")
+    return NormOut(h_out, out, out_sf, x, r1, r2, yc, yc_sf, hc, hc_sf)
+
+
+def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h_sf=None,
+                                  saved_y=None, saved_y_sf=None, rstd_post=None, w_post=None,
+                                  gate=None, residual_scale=1.0, weight_offset=0.0, fmt="e4m3",
+                                  group=128, clamp_min=0.0, sf_flags=0, want_dy=False,
+                                  want_codes=True, stream=None):
+    """Gradient of qcast_norm_per_token (include/qcast.h) from ``dx``, the
+    gradient of its cast input, and ``dh``, the gradient of the residual stream
+    (None: zero). ``saved_h``/``saved_y``: the bf16 residual stream and block
+    output, or their 8-bit checkpoints with ``saved_h_sf``/``saved_y_sf``.
+
+    Returns a ``NormGrad``: ``dh`` the gradient of the residual input,
+    ``out``/``out_sf`` the per-token cast of the block output's gradient (with
+    ``want_codes``), ``dy`` the same in bf16 (with ``want_dy``), ``dw_post`` and
+    ``dw_pre`` fp32, and ``dgate`` in the gate's shape (fp32; bf16 for a
+    ``[rows, cols]`` gate)."""
+    f = fmt_id(fmt)
+    dx = _bf16_input(dx, "dx")
+    rows, cols = dx.shape
+    dev = dx.device
+    bf16, f32 = torch.bfloat16, torch.float32
+    dhptr = None if dh is None else _like(dh, (rows, cols), bf16, dev, "dh")
+    sf = 0
+    if saved_h_sf is None:
+        shptr, shsf = _like(saved_h, (rows, cols), bf16, dev, "saved_h"), None
+    else:
+        sf = _codes(saved_h, "saved_h")
+        shptr = _like(saved_h, (rows, cols), saved_h.dtype, dev, "saved_h")
+        shsf = _like(saved_h_sf, (rows, cols // 128), f32, dev, "saved_h_sf")
+    syptr = sysf = None
+    if saved_y is not None:
+        syptr = _like(saved_y, (rows, cols), saved_h.dtype, dev, "saved_y")
+        if sf:
+            sysf = _like(saved_y_sf, (rows, cols // 128), f32, dev, "saved_y_sf")
+    elif w_post is not None or gate is not None:
+        raise QcastError(1, "w_post and gate need saved_y")
+    if saved_y_sf is not None and (not sf or saved_y is None):
+        raise QcastError(1, "saved_y_sf needs saved_y and saved_h in 8 bits")
+    r2ptr = _like(rstd_pre, (rows,), f32, dev, "rstd_pre")
+    wqptr = _like(w_pre, (cols,), bf16, dev, "w_pre")
+    if (w_post is None) != (rstd_post is None):
+        raise QcastError(1, "w_post and rstd_post come together")
+    wpptr = None if w_post is None else _like(w_post, (cols,), bf16, dev, "w_post")
+    r1ptr = None if rstd_post is None else _like(rstd_post, (rows,), f32, dev, "rstd_post")
+    kind, gptr = _gate_arg(gate, rows, cols, dev)
+    stream_handle, ctx = _placed(dev, stream)
+    with ctx:
+        dh_out = torch.empty((rows, cols), dtype=bf16, device=dev)
+        out = out_sf = dy = dw_post = dgate = ws = None
+        if saved_y is not None:
+            if want_codes:
+                out = torch.empty(code_shape(f, rows, cols), dtype=_code_dtype(f), device=dev)
+                shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
+                out_sf = torch.empty(shape, dtype=dt, device=dev)
+            if want_dy:
+                dy = torch.empty((rows, cols), dtype=bf16, device=dev)
+        dw_pre = torch.empty(cols, dtype=f32, device=dev)
+        if w_post is not None:
+            dw_post = torch.empty(cols, dtype=f32, device=dev)
+        if kind:
+            dgate = torch.empty(gate.shape, dtype=bf16 if kind == GATE_FULL else f32, device=dev)
+        if rows > 1:
+            ws = torch.empty(min(rows, NORM_WS_ROWS) * 3 * cols, dtype=f32, device=dev)
+        check(load().qcast_norm_backward_per_token(
+            dx.data_ptr(), dhptr, rows, cols, sf, shptr, shsf, syptr, sysf, r1ptr, r2ptr, wpptr,
+            wqptr, gptr, kind, residual_scale, weight_offset, f, group, clamp_min, sf_flags,
+            dh_out.data_ptr(), _ptr(out), _ptr(out_sf), _ptr(dy), _ptr(dw_post),
+            dw_pre.data_ptr(), _ptr(dgate), _ptr(ws), stream_handle),
+            "qcast_norm_backward_per_token")
+    return NormGrad(dh_out, out, out_sf, dy, dw_post, dw_pre, dgate)
 
 
 def qcast_abi_version():

@@ -18,6 +18,11 @@ OUT_F32 = 2
 SF_ROUND_POW2 = 1
 SF_COL_MAJOR = 2
 SF_PACKED_UE8M0 = 4
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_TOKEN = 2
+GATE_FULL = 3
+NORM_WS_ROWS = 512          # QCAST_NORM_WS_ROWS
 _FMT = {"e4m3": FMT_E4M3, "e2m1": FMT_E2M1, "e5m2": FMT_E5M2, "e5m6": FMT_E5M6}
 
 _lib = None
@@ -77,6 +82,16 @@ def load():
                                           vp, vp],
         "qcast_swiglu_backward_per_token_sf": [vp, vp, i64, i64, vp, i32, i32, f32, i32, f32, vp,
                                                vp, vp],
+        "qcast_swiglu_checkpoint": [vp, i64, i64, vp, i32, i32, f32, i32, f32, vp, vp, i32, vp,
+                                    vp, vp],
+        "qcast_swiglu_backward_checkpoint": [vp, vp, vp, i64, i64, vp, i32, i32, i32, f32, i32,
+                                             f32] + [vp] * 9,
+        "qcast_recast_per_channel_T": [vp, vp, i64, i64, i32, i32, i32, i32, f32, i32, vp, vp,
+                                       vp],
+        "qcast_norm_per_token": [vp, vp, i64, i64, vp, vp, vp, i32, f32, f32, f32, i32, i32, f32,
+                                 i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp],
+        "qcast_norm_backward_per_token": [vp, vp, i64, i64, i32] + [vp] * 9 +
+                                         [i32, f32, f32, i32, i32, f32, i32] + [vp] * 9,
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -112,6 +127,8 @@ EXPORTS = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_swiglu_backward_per_token", "qcast_swiglu_per_channel_T", "qcast_per_channel",
            "qcast_swiglu_per_token_noalloc", "qcast_per_block_sf", "qcast_per_channel_sf",
            "qcast_per_channel_T_sf", "qcast_swiglu_per_channel_T_sf",
-           "qcast_swiglu_backward_per_token_sf", "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
+           "qcast_swiglu_backward_per_token_sf", "qcast_swiglu_checkpoint",
+           "qcast_swiglu_backward_checkpoint", "qcast_recast_per_channel_T",
+           "qcast_norm_per_token", "qcast_norm_backward_per_token", "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
            "qcast_bench_copy", "qcast_bench_check_scale", "qcast_bench_time_next",
            "qcast_bench_per_channel_T_traffic"]

@@ -155,6 +155,36 @@ int check_swiglu_ex(const void* h, int64_t rows, int64_t cols, const float* row_
   return QCAST_OK;
 }
 
+bool fp8_fmt(int fmt) { return fmt == QCAST_FMT_E4M3 || fmt == QCAST_FMT_E5M2; }
+
+bool finite_value(float v) { return v == v && v >= -3.4028235e38f && v <= 3.4028235e38f; }
+
+// QCAST_OK where there is a device to launch on.
+int device_ok() {
+  qcast::LaunchCaps caps;
+  return caps_for_current_device(&caps);
+}
+
+static_assert(QCAST_NORM_MAX_COLS == 8 * qcast::kNormMaxChunks, "longest row of the norms");
+static_assert(QCAST_NORM_WS_ROWS == qcast::kNormParts, "workspace rows of the norms");
+
+// The scalar arguments of the norm entry points; `saved_fmt` is the format
+// of 8-bit checkpoints, 0 for none.
+int check_norm(int64_t rows, int64_t cols, int fmt, int group, float clamp_min, int sf_flags,
+               int gate_kind, float residual_scale, float weight_offset, int saved_fmt) {
+  if (!any_fmt(fmt) || (saved_fmt != 0 && !fp8_fmt(saved_fmt))) return QCAST_ERR_FORMAT;
+  if (!sf_flags_ok(sf_flags)) return QCAST_ERR_FORMAT;
+  if (!per_token_group_ok(group)) return QCAST_ERR_GROUP;
+  if (rows < 0 || cols < 0 || cols % group != 0 || cols > QCAST_NORM_MAX_COLS ||
+      rows >= (int64_t(1) << 31) || (saved_fmt != 0 && cols % 128 != 0) ||
+      !sf_shape_ok(rows, cols, group, sf_flags))
+    return QCAST_ERR_SHAPE;
+  if (!clamp_min_ok(clamp_min) || !finite_value(residual_scale) || !finite_value(weight_offset) ||
+      gate_kind < QCAST_GATE_NONE || gate_kind > QCAST_GATE_FULL)
+    return QCAST_ERR_VALUE;
+  return QCAST_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -436,6 +466,227 @@ int qcast_cast_back(const void* q, const float* sf, int64_t rows, int64_t cols, 
   if (rc != QCAST_OK) return rc;
   return finish(qcast::launch_cast_back(q, sf, rows, cols, fmt, group, out_dtype == QCAST_OUT_BF16,
                                         out, static_cast<hipStream_t>(stream), caps));
+}
+
+int qcast_swiglu_checkpoint(const void* h, int64_t rows, int64_t cols, const float* row_weight,
+                            int fmt, int group, float clamp_min, int sf_flags, float swiglu_clamp,
+                            void* q, void* sf, int ckpt_fmt, void* ckpt, float* ckpt_sf,
+                            void* stream) {
+  bool empty;
+  const int rc = check_swiglu_ex(h, rows, cols, row_weight, fmt, group, clamp_min, sf_flags,
+                                 swiglu_clamp, q, sf, nullptr, nullptr, &empty);
+  if (!fp8_fmt(ckpt_fmt)) return QCAST_ERR_FORMAT;
+  if (rc != QCAST_OK) return rc;
+  if (!sf_shape_ok(rows, 2 * cols, group, 0)) return QCAST_ERR_SHAPE;
+  if (empty) return QCAST_OK;
+  if (!ckpt || !ckpt_sf) return QCAST_ERR_NULL;
+  if (!aligned(ckpt, 16) || !aligned(ckpt_sf, 4)) return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  return finish(qcast::launch_swiglu_checkpoint(
+      h, rows, cols, row_weight, group, clamp_value(swiglu_clamp),
+      qcast::make_row_cast(rows, cols, fmt, group, floor_for(fmt, clamp_min), (uint32_t)sf_flags,
+                           q, sf),
+      qcast::make_row_cast(rows, 2 * cols, ckpt_fmt, group, default_floor(ckpt_fmt), 0, ckpt,
+                           ckpt_sf),
+      static_cast<hipStream_t>(stream)));
+}
+
+int qcast_swiglu_backward_checkpoint(const void* ckpt, const float* ckpt_sf, const void* dv,
+                                     int64_t rows, int64_t cols, const float* row_weight,
+                                     int ckpt_fmt, int fmt, int group, float clamp_min,
+                                     int sf_flags, float swiglu_clamp, void* q, void* sf,
+                                     void* dhT, void* dhT_sf, void* vT, void* vT_sf, float* dw,
+                                     void* ws, void* stream) {
+  if (!fp8_fmt(fmt) || !fp8_fmt(ckpt_fmt)) return QCAST_ERR_FORMAT;
+  if (!sf_flags_ok(sf_flags)) return QCAST_ERR_FORMAT;
+  if (group != 128) return QCAST_ERR_GROUP;
+  if (rows < 0 || cols < 0 || cols % 128 != 0 || too_big(rows, 2 * cols) ||
+      !qcast::tile_fits(rows, cols, 2 * cols))
+    return QCAST_ERR_SHAPE;
+  const int64_t rows_T = (rows + 127) / 128 * 128;
+  if (sf_flags & QCAST_SF_PACKED_UE8M0) {
+    if ((cols / 128) % 4 != 0 || ((dhT || vT) && (rows_T / 128) % 4 != 0)) return QCAST_ERR_SHAPE;
+  }
+  if (swiglu_clamp != swiglu_clamp) return QCAST_ERR_VALUE;
+  if (!clamp_min_ok(clamp_min)) return QCAST_ERR_VALUE;
+  if (rows == 0 || cols == 0) {
+    if (rows == 0 || !dw) return QCAST_OK;
+    return QCAST_ERR_SHAPE;                       // dw over no columns
+  }
+  if (!ckpt || !ckpt_sf || !dv || !q || !sf || (dhT != nullptr) != (dhT_sf != nullptr) ||
+      (vT != nullptr) != (vT_sf != nullptr) || (dw && cols > 128 && !ws))
+    return QCAST_ERR_NULL;
+  if (!aligned(ckpt, 16) || !aligned(ckpt_sf, 4) || !aligned(dv, 16) || !aligned(q, 16) ||
+      !aligned(sf, 4) || !aligned(row_weight, 4) || !aligned(dhT, 16) || !aligned(dhT_sf, 4) ||
+      !aligned(vT, 16) || !aligned(vT_sf, 4) || !aligned(dw, 4) || !aligned(ws, 16))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::SwigluTile p{};
+  p.ckpt = static_cast<const uint8_t*>(ckpt);
+  p.ckpt_sf = ckpt_sf;
+  p.dv = static_cast<const uint16_t*>(dv);
+  p.w = row_weight;
+  p.q = static_cast<uint8_t*>(q);
+  p.sf = sf;
+  p.lay = qcast::make_sf_layout(rows, 2 * cols, 128, (uint32_t)sf_flags);
+  p.dh = qcast::TileCast{static_cast<uint8_t*>(dhT), dhT_sf,
+                         qcast::make_sf_layout(2 * cols, rows_T, 128, (uint32_t)sf_flags)};
+  p.v = qcast::TileCast{static_cast<uint8_t*>(vT), vT_sf,
+                        qcast::make_sf_layout(cols, rows_T, 128, (uint32_t)sf_flags)};
+  p.dw = dw;
+  p.ws = static_cast<float*>(ws);
+  p.floor = floor_for(fmt, clamp_min);
+  p.clamp = clamp_value(swiglu_clamp);
+  p.rows = (uint32_t)rows;
+  p.cols = (uint32_t)cols;
+  return finish(qcast::launch_swiglu_backward_checkpoint(p, ckpt_fmt, fmt,
+                                                         static_cast<hipStream_t>(stream)));
+}
+
+int qcast_recast_per_channel_T(const void* q_in, const float* sf_in, int64_t rows, int64_t cols,
+                               int in_fmt, int in_group, int fmt, int group, float clamp_min,
+                               int sf_flags, void* qT, void* sf, void* stream) {
+  if (!fp8_fmt(in_fmt) || !fp8_fmt(fmt)) return QCAST_ERR_FORMAT;
+  if (!sf_flags_ok(sf_flags)) return QCAST_ERR_FORMAT;
+  if (!per_token_group_ok(in_group) || group != 128) return QCAST_ERR_GROUP;
+  if (rows < 0 || cols < 0 || cols % in_group != 0 || too_big(rows, cols) ||
+      !qcast::tile_fits(rows, cols, cols))
+    return QCAST_ERR_SHAPE;
+  const int64_t rows_T = (rows + 127) / 128 * 128;
+  if ((sf_flags & QCAST_SF_PACKED_UE8M0) && (rows_T / 128) % 4 != 0) return QCAST_ERR_SHAPE;
+  if (!clamp_min_ok(clamp_min)) return QCAST_ERR_VALUE;
+  if (rows == 0 || cols == 0) return QCAST_OK;
+  if (!q_in || !sf_in || !qT || !sf) return QCAST_ERR_NULL;
+  if (!aligned(q_in, 16) || !aligned(sf_in, 4) || !aligned(qT, 16) || !aligned(sf, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::RecastTile p{};
+  p.q = static_cast<const uint8_t*>(q_in);
+  p.sf = sf_in;
+  p.out = qcast::TileCast{static_cast<uint8_t*>(qT), sf,
+                          qcast::make_sf_layout(cols, rows_T, 128, (uint32_t)sf_flags)};
+  p.floor = floor_for(fmt, clamp_min);
+  p.shift = in_group == 32 ? 2 : in_group == 64 ? 3 : 4;
+  p.rows = (uint32_t)rows;
+  p.cols = (uint32_t)cols;
+  return finish(qcast::launch_recast(p, in_fmt, fmt, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t cols,
+                         const void* w_post, const void* w_pre, const void* gate, int gate_kind,
+                         float residual_scale, float weight_offset, float eps, int fmt, int group,
+                         float clamp_min, int sf_flags, void* h_out, void* q, void* sf,
+                         void* x_out, float* rstd_post, float* rstd_pre, int ckpt_fmt,
+                         void* y_ckpt, float* y_ckpt_sf, void* h_ckpt, float* h_ckpt_sf,
+                         void* stream) {
+  const bool ckpt = y_ckpt || y_ckpt_sf || h_ckpt || h_ckpt_sf;
+  int rc = check_norm(rows, cols, fmt, group, clamp_min, sf_flags, gate_kind, residual_scale,
+                      weight_offset, ckpt ? ckpt_fmt : 0);
+  if (rc != QCAST_OK) return rc;
+  if (!(eps >= 0.0f) || !finite_value(eps)) return QCAST_ERR_VALUE;
+  if (!y && residual_scale != 1.0f) return QCAST_ERR_VALUE;
+  if (rows == 0 || cols == 0) return QCAST_OK;
+  if (!h || !w_pre || (q != nullptr) != (sf != nullptr) || (!q && !x_out) ||
+      (gate != nullptr) != (gate_kind != QCAST_GATE_NONE) || (y != nullptr) != (h_out != nullptr) ||
+      (!y && (w_post || gate || y_ckpt)) || (!w_post && rstd_post) ||
+      (y_ckpt != nullptr) != (y_ckpt_sf != nullptr) ||
+      (h_ckpt != nullptr) != (h_ckpt_sf != nullptr))
+    return QCAST_ERR_NULL;
+  if (!aligned(y, 16) || !aligned(h, 16) || !aligned(w_post, 16) || !aligned(w_pre, 16) ||
+      !aligned(gate, gate_kind == QCAST_GATE_TOKEN ? 4 : 16) || !aligned(h_out, 16) ||
+      !aligned(q, 16) || !aligned(sf, 4) || !aligned(x_out, 16) || !aligned(rstd_post, 4) ||
+      !aligned(rstd_pre, 4) || !aligned(y_ckpt, 16) || !aligned(y_ckpt_sf, 4) ||
+      !aligned(h_ckpt, 16) || !aligned(h_ckpt_sf, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::NormForward p{};
+  p.y = static_cast<const uint16_t*>(y);
+  p.h = static_cast<const uint16_t*>(h);
+  p.w_post = static_cast<const uint16_t*>(w_post);
+  p.w_pre = static_cast<const uint16_t*>(w_pre);
+  p.gate = gate;
+  p.h_out = static_cast<uint16_t*>(h_out);
+  p.x_out = static_cast<uint16_t*>(x_out);
+  p.rstd_post = rstd_post;
+  p.rstd_pre = rstd_pre;
+  p.cast = qcast::make_row_cast(rows, cols, fmt, group, floor_for(fmt, clamp_min),
+                                (uint32_t)sf_flags, q, sf);
+  p.y_ckpt = qcast::make_row_cast(rows, cols, ckpt_fmt, 128, default_floor(ckpt_fmt), 0, y_ckpt,
+                                  y_ckpt_sf);
+  p.h_ckpt = qcast::make_row_cast(rows, cols, ckpt_fmt, 128, default_floor(ckpt_fmt), 0, h_ckpt,
+                                  h_ckpt_sf);
+  p.gate_kind = gate_kind;
+  p.alpha = residual_scale;
+  p.offset = weight_offset;
+  p.eps = eps;
+  p.n = (float)cols;
+  p.chunks = (uint32_t)(cols / 8);
+  return finish(qcast::launch_norm(p, rows, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t rows, int64_t cols,
+                                  int saved_fmt, const void* saved_h, const float* saved_h_sf,
+                                  const void* saved_y, const float* saved_y_sf,
+                                  const float* rstd_post, const float* rstd_pre,
+                                  const void* w_post, const void* w_pre, const void* gate,
+                                  int gate_kind, float residual_scale, float weight_offset,
+                                  int fmt, int group, float clamp_min, int sf_flags,
+                                  void* dh_out, void* q, void* sf, void* dy_out, float* dw_post,
+                                  float* dw_pre, void* dgate, void* ws, void* stream) {
+  const int rc = check_norm(rows, cols, fmt, group, clamp_min, sf_flags, gate_kind,
+                            residual_scale, weight_offset, saved_fmt);
+  if (rc != QCAST_OK) return rc;
+  if (cols == 0) return QCAST_OK;
+  const bool saved8 = saved_fmt != 0;
+  if (rows > 0) {
+    if (!dx || !saved_h || !rstd_pre || !w_pre || !dh_out || (saved8 && !saved_h_sf) ||
+        (!saved8 && (saved_h_sf || saved_y_sf)) || (saved8 && (saved_y != nullptr) !=
+        (saved_y_sf != nullptr)) || (rstd_post != nullptr) != (w_post != nullptr) ||
+        (gate != nullptr) != (gate_kind != QCAST_GATE_NONE) ||
+        (q != nullptr) != (sf != nullptr) || (saved_y && !q && !dy_out) ||
+        (!saved_y && (w_post || gate || q || dy_out)) || (rows > 1 && !ws))
+      return QCAST_ERR_NULL;
+  }
+  if ((dw_post && !w_post) || (dgate && !gate)) return QCAST_ERR_NULL;
+  const int gate_align = gate_kind == QCAST_GATE_TOKEN ? 4 : 16;
+  if (!aligned(dx, 16) || !aligned(dh_in, 16) || !aligned(saved_h, 16) ||
+      !aligned(saved_h_sf, 4) || !aligned(saved_y, 16) || !aligned(saved_y_sf, 4) ||
+      !aligned(rstd_post, 4) || !aligned(rstd_pre, 4) || !aligned(w_post, 16) ||
+      !aligned(w_pre, 16) || !aligned(gate, gate_align) || !aligned(dh_out, 16) ||
+      !aligned(q, 16) || !aligned(sf, 4) || !aligned(dy_out, 16) || !aligned(dw_post, 16) ||
+      !aligned(dw_pre, 16) || !aligned(dgate, gate_align) || !aligned(ws, 16))
+    return QCAST_ERR_ALIGN;
+  const bool channel = gate_kind == QCAST_GATE_CHANNEL;
+  if (rows == 0 && !dw_pre && !dw_post && !(channel && dgate)) return QCAST_OK;
+  if (const int drc = device_ok()) return drc;
+  qcast::NormBackward p{};
+  p.dx = static_cast<const uint16_t*>(dx);
+  p.dh_in = static_cast<const uint16_t*>(dh_in);
+  p.saved_h = saved_h;
+  p.saved_h_sf = saved_h_sf;
+  p.saved_y = saved_y;
+  p.saved_y_sf = saved_y_sf;
+  p.rstd_pre = rstd_pre;
+  p.rstd_post = rstd_post;
+  p.w_post = static_cast<const uint16_t*>(w_post);
+  p.w_pre = static_cast<const uint16_t*>(w_pre);
+  p.gate = gate;
+  p.dh_out = static_cast<uint16_t*>(dh_out);
+  p.dy_out = static_cast<uint16_t*>(dy_out);
+  p.sums[0] = dw_pre;
+  p.sums[1] = dw_post;
+  p.sums[2] = channel ? static_cast<float*>(dgate) : nullptr;
+  p.dgate = dgate;
+  p.ws = static_cast<float*>(ws);
+  p.cast = qcast::make_row_cast(rows, cols, fmt, group, floor_for(fmt, clamp_min),
+                                (uint32_t)sf_flags, q, sf);
+  p.saved_fmt = saved_fmt;
+  p.gate_kind = gate_kind;
+  p.alpha = residual_scale;
+  p.offset = weight_offset;
+  p.n = (float)cols;
+  p.chunks = (uint32_t)(cols / 8);
+  return finish(qcast::launch_norm_backward(p, rows, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -121,4 +121,116 @@ hipError_t launch_cast_back(const void* q, const float* sf, int64_t rows, int64_
                             int group, bool out_bf16, void* out, hipStream_t stream,
                             const LaunchCaps& caps);
 
+// A per-token cast whose format and group are fixed for a launch.
+struct RowCast {
+  uint8_t* q;      // codes; null: nothing is cast
+  void* sf;        // scales in the layout lay
+  SfLayout lay;
+  float floor;
+  int fmt;         // Fmt
+  int shift;       // log2 of the lanes of a group (group = 8 << shift)
+};
+inline RowCast make_row_cast(int64_t rows, int64_t cols, int fmt, int group, float floor,
+                             uint32_t sf_flags, void* q, void* sf) {
+  return RowCast{static_cast<uint8_t*>(q), sf, make_sf_layout(rows, cols, group, sf_flags), floor,
+                 fmt, group == 32 ? 2 : group == 64 ? 3 : 4};
+}
+
+// As launch_swiglu_per_token (without a counter), and the per-token codes of
+// h itself in ckpt (8-bit format, same group, row-major scales).
+hipError_t launch_swiglu_checkpoint(const void* h, int64_t rows, int64_t cols, const float* w,
+                                    int group, float swiglu_clamp, const RowCast& cast,
+                                    const RowCast& ckpt, hipStream_t stream);
+
+// What the tile kernels (128 tokens x 128 channels) are called with: one
+// transposed cast of 128-token groups, rows padded to whole groups.
+struct TileCast {
+  uint8_t* qT;     // [channels][rows_T] 8-bit codes; null: not written
+  void* sf;
+  SfLayout lay;    // rows = channels, groups = rows_T / 128
+};
+struct SwigluTile {
+  const uint8_t* ckpt;       // [rows, 2*cols] codes of (gate | up)
+  const float* ckpt_sf;      // [rows, 2*cols/128]
+  const uint16_t* dv;        // [rows, cols] bf16
+  const float* w;            // [rows] or null
+  uint8_t* q;                // [rows, 2*cols] codes of [dg | du]
+  void* sf;
+  SfLayout lay;              // of the rows [dg | du]
+  TileCast dh, v;            // transposed [dg | du] and v
+  float* dw;                 // [rows] or null
+  float* ws;                 // [cols/128][rows] partial sums of dw
+  float floor;
+  float clamp;               // 0: none
+  uint32_t rows, cols;
+};
+hipError_t launch_swiglu_backward_checkpoint(const SwigluTile& p, int ckpt_fmt, int fmt,
+                                             hipStream_t stream);
+
+struct RecastTile {
+  const uint8_t* q;          // [rows, cols] codes
+  const float* sf;           // [rows, cols / (8 << shift)]
+  TileCast out;
+  float floor;
+  int shift;                 // log2(in_group / 8)
+  uint32_t rows, cols;
+};
+hipError_t launch_recast(const RecastTile& p, int in_fmt, int fmt, hipStream_t stream);
+
+// Whether the tile kernels' 32-bit tile counts and in-tile offsets hold for
+// rows x cols values read from rows of `stride` elements.
+bool tile_fits(int64_t rows, int64_t cols, int64_t stride);
+
+// The norms around a block (norm.hip, norm_backward.hip).
+enum GateKind : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+constexpr uint32_t kNormMaxChunks = 4096;      // 32768 columns: 1024 threads x 4 chunks of 8
+constexpr int64_t kNormParts = 512;            // workgroups of the backward pass
+
+struct NormForward {
+  const uint16_t* y;         // or null
+  const uint16_t* h;
+  const uint16_t* w_post;    // or null
+  const uint16_t* w_pre;
+  const void* gate;          // by gate_kind
+  uint16_t* h_out;
+  uint16_t* x_out;           // or null
+  float* rstd_post;          // or null
+  float* rstd_pre;           // or null
+  RowCast cast, y_ckpt, h_ckpt;
+  int gate_kind;
+  float alpha, offset, eps;
+  float n;                   // cols
+  uint32_t chunks;           // cols / 8
+};
+hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream);
+
+struct NormSums {
+  float* p[3];               // [cols] each, or null
+};
+struct NormBackward {
+  const uint16_t* dx;
+  const uint16_t* dh_in;     // or null
+  const void* saved_h;       // bf16, or 8-bit codes with scales
+  const float* saved_h_sf;
+  const void* saved_y;       // or null
+  const float* saved_y_sf;
+  const float* rstd_pre;
+  const float* rstd_post;    // null without w_post
+  const uint16_t* w_post;    // or null
+  const uint16_t* w_pre;
+  const void* gate;
+  uint16_t* dh_out;
+  uint16_t* dy_out;          // or null
+  float* sums[3];            // dw_pre, dw_post, dgate of a channel gate; each may be null
+  void* dgate;               // of a token or full gate, or null
+  float* ws;                 // [min(rows, kNormParts)][3][cols]
+  RowCast cast;
+  int saved_fmt;             // 0: bf16
+  int gate_kind;
+  float alpha, offset;
+  float n;
+  uint32_t chunks;
+};
+hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, hipStream_t stream);
+
 }  // namespace qcast

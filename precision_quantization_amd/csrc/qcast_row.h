@@ -1,0 +1,147 @@
+// qcast_row.h -- device helpers of the kernels that hold a whole row, or a
+// 128 x 128 tile, of fp32 values in registers before they cast it: wave and
+// workgroup sums, 8-bit decoding, and the per-token cast of an 8-column chunk
+// with the group size and the format chosen at run time.
+//
+// Decoding and encoding are the conversions of qcast_device.h; a decoded
+// value is the fp32 product code * sf, as cast_back forms it.
+#pragma once
+
+#include "qcast_device.h"
+
+namespace qcast {
+
+// Sums over the wave64: every lane ends with the same bits (each step adds a
+// pair of lanes' values, and fp32 addition commutes).
+template <int kCtrl>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(dpp<kCtrl>(__float_as_uint(v)));
+}
+// Sum over aligned runs of 16 lanes.
+__device__ __forceinline__ float row16_sum(float v) {
+  v = add_dpp<kDppXor1>(v);
+  v = add_dpp<kDppXor2>(v);
+  v = add_dpp<kDppHalfMirror>(v);
+  return add_dpp<kDppMirror>(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  const uint32_t b = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  v = __uint_as_float((uint32_t)r[0]) + __uint_as_float((uint32_t)r[1]);
+  const uint32_t c = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return __uint_as_float((uint32_t)s[0]) + __uint_as_float((uint32_t)s[1]);
+}
+
+// Abs-max over the aligned run of 2^shift lanes (4, 8 or 16; shift is the
+// same in every lane).
+__device__ __forceinline__ float run_max(float m, int shift) {
+  uint32_t b = __float_as_uint(m);
+  b = umax(b, dpp<kDppXor1>(b));
+  b = umax(b, dpp<kDppXor2>(b));
+  if (shift >= 3) b = umax(b, dpp<kDppHalfMirror>(b));
+  if (shift >= 4) b = umax(b, dpp<kDppMirror>(b));
+  return __uint_as_float(b);
+}
+
+// Four 8-bit codes of a word -> four fp32 (exact).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int kFmt>
+__device__ __forceinline__ void decode4(uint32_t w, float v[4]) {
+  static_assert(kFmt == kE4M3 || kFmt == kE5M2, "8-bit formats only");
+  f32x2 lo, hi;
+  if constexpr (kFmt == kE4M3) {
+    lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  } else {
+    lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false);
+    hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, true);
+  }
+  v[0] = lo.x;
+  v[1] = lo.y;
+  v[2] = hi.x;
+  v[3] = hi.y;
+}
+template <int kFmt>
+__device__ __forceinline__ void decode8(const u32x2& w, float sf, float v[8]) {
+  decode4<kFmt>(w.x, v);
+  decode4<kFmt>(w.y, v + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = v[i] * sf;
+}
+
+// Two fp32 -> two bf16 (nearest even) in one dword (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(a));
+  const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(b));
+  return lo | (hi << 16);
+}
+__device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
+  return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+               pack_bf16(v[6], v[7])};
+}
+
+// Store the scale of group kr of row r, held by the 2^shift lanes of the
+// group (store_row_group_scale with the run length at run time).
+__device__ __forceinline__ void store_run_scale(void* sf, uint32_t r, uint32_t kr, const Scale& s,
+                                                const SfLayout& lay, int shift) {
+  const int lane = threadIdx.x & 63;
+  const bool col = (lay.flags & kSfColMajor) != 0;
+  if (lay.flags & kSfPacked) {
+    const int n = 1 << shift;
+    const uint32_t e = __float_as_uint(s.sf) >> 23;
+    const uint32_t w = e | ((uint32_t)__shfl((int)e, lane + n) << 8) |
+                       ((uint32_t)__shfl((int)e, lane + 2 * n) << 16) |
+                       ((uint32_t)__shfl((int)e, lane + 3 * n) << 24);
+    if ((lane & (4 * n - 1)) == 0) {
+      const uint32_t idx = col ? (kr / 4) * lay.rows_pad + r : r * (lay.gpr / 4) + kr / 4;
+      static_cast<uint32_t*>(sf)[idx] = w;
+    }
+  } else if ((lane & ((1 << shift) - 1)) == 0) {
+    static_cast<float*>(sf)[col ? kr * lay.rows_pad + r : r * lay.gpr + kr] = s.sf;
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void cast_chunk_fmt(const RowCast& rc, uint32_t row, uint32_t jc,
+                                               uint32_t chunks, float amax, const float v[8]) {
+  Scale s = group_scale<kFmt>(amax, rc.floor);
+  if (rc.lay.flags & kSfRound) s = round_scale_pow2(s);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = v[i] * s.inv;
+  store_chunk8<kFmt>(rc.q, (int64_t)row * chunks + jc, y);
+  store_run_scale(rc.sf, row, jc >> rc.shift, s, rc.lay, rc.shift);
+}
+
+// Cast chunk jc (columns 8 jc .. 8 jc + 7) of row `row` (of `chunks` chunks).
+// The lanes of a scale group call this together, lane = jc mod 64.
+__device__ __forceinline__ void cast_chunk(const RowCast& rc, uint32_t row, uint32_t jc,
+                                           uint32_t chunks, const float v[8]) {
+  const float amax = run_max(absmax8(v), rc.shift);
+  switch (rc.fmt) {
+    case kE4M3: cast_chunk_fmt<kE4M3>(rc, row, jc, chunks, amax, v); break;
+    case kE5M2: cast_chunk_fmt<kE5M2>(rc, row, jc, chunks, amax, v); break;
+    case kE2M1: cast_chunk_fmt<kE2M1>(rc, row, jc, chunks, amax, v); break;
+    default: cast_chunk_fmt<kE5M6>(rc, row, jc, chunks, amax, v); break;
+  }
+}
+
+// The same into one of the two 8-bit formats with plain row-major scales (a
+// checkpoint).
+__device__ __forceinline__ void checkpoint_chunk(const RowCast& rc, uint32_t row, uint32_t jc,
+                                                 uint32_t chunks, const float v[8]) {
+  const float amax = run_max(absmax8(v), rc.shift);
+  const bool e4 = rc.fmt == kE4M3;
+  const Scale s = e4 ? group_scale<kE4M3>(amax, rc.floor) : group_scale<kE5M2>(amax, rc.floor);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = v[i] * s.inv;
+  if (e4) store_chunk8<kE4M3>(rc.q, (int64_t)row * chunks + jc, y);
+  else store_chunk8<kE5M2>(rc.q, (int64_t)row * chunks + jc, y);
+  if ((threadIdx.x & ((1 << rc.shift) - 1)) == 0)
+    static_cast<float*>(rc.sf)[(int64_t)row * rc.lay.gpr + (jc >> rc.shift)] = s.sf;
+}
+
+}  // namespace qcast

@@ -1,0 +1,66 @@
+// qcast_tile.h -- what the kernels on tiles of 128 tokens x 128 channels
+// share: the walk over the tiles, the LDS tile in which 8-bit codes are
+// transposed, and the scales of the 128 channels.
+//
+// Codes wait in LDS as rows of 128 tokens (32 dwords) per channel, a dword
+// holding 4 consecutive tokens. The dword index is XOR-swizzled in whole
+// 16-byte groups by the channel, so that lanes writing the same tokens of
+// different channels spread over the banks and a 16-byte run of tokens stays
+// contiguous for the read-back.
+#pragma once
+
+#include "qcast_device.h"
+#include "qcast_kernels.h"
+
+namespace qcast {
+
+constexpr uint32_t kTile = 128;              // tokens and channels of a tile
+constexpr uint32_t kTileXcds = 8;
+
+// Tile walk: each XCD takes a contiguous range of tiles, token groups
+// fastest, so neighbouring tokens' lines of one channel row meet in one L2.
+struct TileWalk {
+  uint32_t ntg, nct, ntiles, per_xcd;
+};
+inline TileWalk make_tile_walk(int64_t rows, int64_t cols) {
+  TileWalk w;
+  w.ntg = (uint32_t)((rows + kTile - 1) / kTile);
+  w.nct = (uint32_t)((cols + kTile - 1) / kTile);
+  w.ntiles = w.ntg * w.nct;
+  w.per_xcd = (w.ntiles + kTileXcds - 1) / kTileXcds;
+  return w;
+}
+
+__device__ __forceinline__ uint32_t swizzled(uint32_t channel, uint32_t dword) {
+  return channel * 32 + (dword ^ (4 * ((channel >> 3) & 7)));
+}
+
+// The scale of one channel over the tile's tokens, formed and stored by one
+// lane; returns what its values are multiplied by.
+template <int kFmt>
+__device__ __forceinline__ float channel_scale(const TileCast& out, uint32_t channel,
+                                               uint32_t group, float amax, float floor) {
+  Scale s = group_scale<kFmt>(amax, floor);
+  if (out.lay.flags & kSfRound) s = round_scale_pow2(s);
+  store_lone_scale(out.sf, channel, group, s, out.lay);
+  return s.inv;
+}
+
+// Store the LDS tile's channel rows [c0, c0 + nc) of token group gt, 16
+// tokens per lane. rows_T: codes per channel row. kN threads call this.
+template <int kN>
+__device__ __forceinline__ void store_tile_rows(const uint32_t* tile, uint8_t* qT, uint32_t c0,
+                                                uint32_t nc, uint32_t gt, uint32_t rows_T) {
+  uint8_t* out = qT + (uint64_t)c0 * rows_T + gt * kTile;
+#pragma unroll
+  for (uint32_t r = 0; r < kTile * 8 / kN; ++r) {
+    const uint32_t idx = threadIdx.x + r * kN;
+    const uint32_t c = idx / 8, v = idx % 8;
+    if (c < nc) {
+      const u32x4 val = *reinterpret_cast<const u32x4*>(tile + swizzled(c, 4 * v));
+      store_stream(reinterpret_cast<u32x4*>(out + c * rows_T + 16 * v), val);
+    }
+  }
+}
+
+}  // namespace qcast

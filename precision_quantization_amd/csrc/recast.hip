@@ -1,0 +1,130 @@
+// recast.hip -- stored per-token 8-bit codes cast again along the tokens and
+// written transposed (the operand of a weight gradient from an activation
+// that the forward pass kept in 8 bits).
+//
+// x[t][c] = decode(code) * sf[t][c / in_group] in fp32; then the per-channel
+// cast over 128 tokens written transposed (per_channel_t.hip), with the last
+// token group filled up with zeros. Going through cast_back and the bf16
+// transposed cast moves 6 bytes per element and rounds to bf16 on the way;
+// this moves 2.
+//
+// gfx950 design. A workgroup owns 128 tokens x 128 channels. A lane loads 16
+// consecutive channels (16 bytes) of 4 consecutive tokens and keeps the
+// codes, not the values: they are decoded once for the maxima and again for
+// the codes, which costs one conversion per two values and saves 64
+// registers. 8 lanes cover a token's 128 channels.
+#include "qcast_device.h"
+#include "qcast_kernels.h"
+#include "qcast_row.h"
+#include "qcast_tile.h"
+
+namespace qcast {
+namespace {
+
+// The fp32 value of code j (0..15) of a token's 16 codes.
+template <int kIn>
+__device__ __forceinline__ void decode_word(uint32_t w, float sf, float v[4]) {
+  decode4<kIn>(w, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = v[i] * sf;
+}
+
+template <int kIn, int kFmt>
+__global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk tw) {
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * 32];
+  __shared__ float amax_s[kThreads / 64][kTile];
+  __shared__ float inv_s[kTile];
+  const uint32_t tau = (blockIdx.x % kTileXcds) * tw.per_xcd + blockIdx.x / kTileXcds;
+  if (tau >= tw.ntiles) return;
+  const uint32_t ct = tau / tw.ntg, gt = tau - ct * tw.ntg;
+  const uint32_t c0 = ct * kTile, t0 = gt * kTile;
+  const uint32_t nc = p.cols - c0 < kTile ? p.cols - c0 : kTile;
+  const uint32_t ch = threadIdx.x & 7;           // 16-channel chunk
+  const uint32_t quad = threadIdx.x >> 3;        // 4 tokens
+  const bool valid_ch = ch * 16 < nc;
+  const uint32_t gpr = p.cols >> (p.shift + 3);
+  u32x4 raw[4];
+  float sf[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = t0 + quad * 4 + i;
+    raw[i] = u32x4{0u, 0u, 0u, 0u};
+    sf[i] = 0.0f;
+    if (valid_ch && t < p.rows) {
+      const uint64_t at = (uint64_t)t * p.cols + c0 + ch * 16;
+      raw[i] = load_stream(reinterpret_cast<const u32x4*>(p.q + at));
+      // 16 channels lie in one group: groups of 32, 64 and 128 are whole chunks
+      sf[i] = p.sf[(uint64_t)t * gpr + ((c0 + ch * 16) >> (p.shift + 3))];
+    }
+  }
+  // column maxima of the lane's 4 tokens, then over the 8 lanes of the wave
+  // that hold the same channels
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[4];
+      decode_word<kIn>(raw[i][w], sf[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], fabsf(v[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t b = __float_as_uint(m[j]);
+      b = umax(b, dpp<kDppRor8>(b));
+      b = max_xor16(b);
+      b = max_xor32(b);
+      if ((threadIdx.x & 63) < 8) amax_s[threadIdx.x >> 6][ch * 16 + 4 * w + j] = __uint_as_float(b);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kTile) {
+    const uint32_t c = threadIdx.x;
+    float m = amax_s[0][c];
+#pragma unroll
+    for (int i = 1; i < kThreads / 64; ++i) m = fmaxf(m, amax_s[i][c]);
+    if (c < nc) inv_s[c] = channel_scale<kFmt>(p.out, c0 + c, gt, m, p.floor);
+  }
+  __syncthreads();
+  if (valid_ch) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) decode_word<kIn>(raw[i][w], sf[i], v[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = ch * 16 + 4 * w + j;
+        const float inv = inv_s[c];
+        tile[swizzled(c, quad)] =
+            fp8x4<kFmt>(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
+      }
+    }
+  }
+  __syncthreads();
+  store_tile_rows<kThreads>(tile, p.out.qT, c0, nc, gt, tw.ntg * kTile);
+}
+
+}  // namespace
+
+bool tile_fits(int64_t rows, int64_t cols, int64_t stride) {
+  const int64_t lim = int64_t(1) << 31;
+  if (rows < 0 || rows >= lim || stride >= lim) return false;
+  const int64_t ntg = (rows + kTile - 1) / kTile;
+  const int64_t nct = (cols + kTile - 1) / kTile;
+  return (nct == 0 || ntg < (lim - 16) / nct) && (int64_t)kTile * stride < lim &&
+         (int64_t)kTile * kTile * ntg < lim;
+}
+
+hipError_t launch_recast(const RecastTile& p, int in_fmt, int fmt, hipStream_t stream) {
+  const TileWalk tw = make_tile_walk(p.rows, p.cols);
+  if (tw.ntiles == 0) return hipSuccess;
+  auto kernel = in_fmt == kE4M3
+                    ? (fmt == kE4M3 ? recast_kernel<kE4M3, kE4M3> : recast_kernel<kE4M3, kE5M2>)
+                    : (fmt == kE4M3 ? recast_kernel<kE5M2, kE4M3> : recast_kernel<kE5M2, kE5M2>);
+  launch_kernel(kernel, dim3(tw.per_xcd * kTileXcds), dim3(kThreads), 0, stream, p, tw);
+  return hipGetLastError();
+}
+
+}  // namespace qcast

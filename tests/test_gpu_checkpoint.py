@@ -1,0 +1,193 @@
+"""The SwiGLU checkpoint, its backward pass and the recast of stored codes:
+against the oracle where the result is defined to the bit, else against the
+64-bit formulas within the bounds of block_ref."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as br
+import oracle
+import precision_quantization_amd as pq
+from precision_quantization_amd import workloads
+
+pytestmark = pytest.mark.gpu
+PACKED, COL, ROUND = pq.SF_PACKED_UE8M0, pq.SF_COL_MAJOR, pq.SF_ROUND_POW2
+F8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.uint8).cpu(), b.view(torch.uint8).cpu())
+
+
+@pytest.mark.parametrize("fmt,group,flags", [("e4m3", 128, 0), ("e5m2", 64, ROUND), ("e2m1", 32, PACKED | COL),
+                                             ("e5m6", 128, COL), ("e4m3", 32, PACKED)])
+@pytest.mark.parametrize("rows,cols,weighted,clamp,ckpt", [(1, 512, False, 0.0, "e4m3"), (67, 1920, True, 2.0, "e5m2"),
+                                                           (257, 128 * 4, True, 0.0, "e4m3")])
+def test_swiglu_checkpoint(dev, fmt, group, flags, rows, cols, weighted, clamp, ckpt):
+    if flags & PACKED and (cols // group) % 4:
+        cols = 512 * 4
+    print(f"swiglu checkpoint {fmt} g{group} flags {flags} {rows}x{cols}", flush=True)
+    wl = workloads.swiglu_input(seed=rows, rows=rows, cols=cols)
+    h, w = wl.x.to(dev), wl.w.to(dev) if weighted else None
+    q, sf, c, csf = pq.qcast_swiglu_checkpoint(h, w, fmt, group, sf_flags=flags, swiglu_clamp=clamp, ckpt_fmt=ckpt)
+    q2, sf2 = pq.qcast_swiglu_per_token_ex(h, w, fmt, group, sf_flags=flags, swiglu_clamp=clamp)
+    cr, csfr = oracle.per_token(workloads.bf16_bits(wl.x), ckpt, group)
+    torch.cuda.synchronize()
+    assert same(q, q2)
+    n = rows if flags & COL else None
+    assert same(sf[:, :n].contiguous(), sf2[:, :n].contiguous())
+    assert np.array_equal(br.raw(c), cr) and np.array_equal(br.raw(csf), csfr)
+
+
+def test_swiglu_checkpoint_of_zero_tiny_and_huge_rows(dev):
+    h = torch.zeros(5, 512)
+    h[1] = -0.0
+    h[2] = 1e-38
+    h[3] = 3e38
+    h[4, ::7] = -1e30
+    h = h.to(torch.bfloat16)
+    for ckpt in ("e4m3", "e5m2"):
+        _, _, c, csf = pq.qcast_swiglu_checkpoint(h.to(dev), ckpt_fmt=ckpt)
+        cr, csfr = oracle.per_token(workloads.bf16_bits(h), ckpt, 128)
+        assert np.array_equal(br.raw(c), cr) and np.array_equal(br.raw(csf), csfr)
+
+
+def check_backward(dev, rows, cols, ckpt, fmt, flags=0, weighted=True, clamp=0.0, transposed=True, weight_grad=True, seed=0):
+    print(f"swiglu backward {ckpt}->{fmt} flags {flags} {rows}x{cols} clamp {clamp}", flush=True)
+    hh, dv, w = workloads.swiglu_grad(seed=seed + rows, rows=rows, cols=cols)
+    w = w if weighted else None
+    codes, scales, h = br.stored(hh, ckpt)
+    r = pq.qcast_swiglu_backward_checkpoint(codes.to(dev), scales.to(dev), dv.to(dev), None if w is None else w.to(dev), fmt,
+                                            sf_flags=flags, swiglu_clamp=clamp, transposed=transposed, weight_grad=weight_grad)
+    torch.cuda.synchronize()
+    args = (h, dv.double(), None if w is None else w.double(), clamp)
+    d, v, dw = br.swiglu_grad(*args)
+    sd, sv, sdw = br.swiglu_grad_slack(*args)
+    br.check_cast(br.raw(r.dh), br.raw(r.dh_sf), d, fmt, 128, sd.numpy(), flags, what="dh")
+    if transposed:
+        pad = -rows % 128
+
+        def t(x):
+            return torch.cat([x, x.new_zeros(pad, x.shape[1])]).t().contiguous().numpy()
+        br.check_cast(br.raw(r.dh_t), br.raw(r.dh_t_sf), t(d), fmt, 128, t(sd), flags, what="dh_t")
+        br.check_cast(br.raw(r.v_t), br.raw(r.v_t_sf), t(v), fmt, 128, t(sv), flags, what="v_t")
+        if pad:
+            assert not br.raw(r.dh_t)[:, rows:].any() and not br.raw(r.v_t)[:, rows:].any()
+    else:
+        assert r.dh_t is None and r.v_t is None and r.dh_t_sf is None
+    if weight_grad:
+        assert ((r.dw.cpu().double() - dw).abs() <= sdw).all()
+    else:
+        assert r.dw is None
+    return r
+
+
+@pytest.mark.parametrize("ckpt,fmt", [("e4m3", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("rows,cols,weighted,clamp", [(1, 128, True, 0.0), (127, 256, False, 0.0), (128, 384, True, 2.0),
+                                                      (129, 128, True, 1.0), (300, 640, False, 3.0)])
+def test_backward(dev, ckpt, fmt, rows, cols, weighted, clamp):
+    check_backward(dev, rows, cols, ckpt, fmt, 0, weighted, clamp)
+
+
+@pytest.mark.parametrize("flags", [ROUND, COL, COL | ROUND, PACKED, PACKED | COL])
+def test_backward_layouts(dev, flags):
+    check_backward(dev, 400, 512, "e4m3", "e4m3", flags)
+
+
+def test_backward_without_the_optional_outputs(dev):
+    a = check_backward(dev, 130, 256, "e4m3", "e4m3", transposed=False, weight_grad=False)
+    b = check_backward(dev, 130, 256, "e4m3", "e4m3")
+    assert same(a.dh, b.dh) and same(a.dh_sf, b.dh_sf)
+
+
+def test_backward_of_zero_gradients(dev):
+    # a token whose gradient or weight is zero gives zero codes and the floor's scale
+    hh, dv, w = workloads.swiglu_grad(seed=3, rows=130, cols=128)
+    dv[5] = 0
+    w[7] = 0
+    codes, scales, h = br.stored(hh, "e4m3")
+    r = pq.qcast_swiglu_backward_checkpoint(codes.to(dev), scales.to(dev), dv.to(dev), w.to(dev))
+    assert not (r.dh.view(torch.uint8)[[5, 7]] & 0x7F).any()
+    assert (r.dh_sf[[5, 7]] == oracle.scale("e4m3", np.float32(0))[0]).all()
+    assert r.dw[5] == 0 and r.dw[7] != 0
+    assert not (r.dh_t.view(torch.uint8)[:, [5, 7]] & 0x7F).any() and not (r.v_t.view(torch.uint8)[:, 7] & 0x7F).any()
+
+
+def check_recast(dev, x, in_fmt, group, fmt, flags=0, clamp_min=0.0):
+    rows, cols = x.shape
+    print(f"recast {in_fmt} g{group} -> {fmt} flags {flags} {rows}x{cols}", flush=True)
+    codes, scales, v = br.stored(x, in_fmt, group)
+    q, sf = pq.qcast_recast_per_channel_T(codes.to(dev), scales.to(dev), fmt, sf_flags=flags, clamp_min=clamp_min)
+    torch.cuda.synchronize()
+    pad = -rows % 128
+    vt = torch.cat([v.float(), torch.zeros(pad, cols)]).t().contiguous().numpy()
+    if flags:
+        br.check_cast(br.raw(q), br.raw(sf), vt, fmt, 128, 0.0, flags, clamp_min, "recast")
+    else:
+        qr, sfr = oracle.per_token_f32(vt, fmt, 128, clamp_min)
+        assert np.array_equal(br.raw(q), qr) and np.array_equal(br.raw(sf), sfr)
+    return q, sf
+
+
+@pytest.mark.parametrize("in_fmt,fmt", [("e4m3", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("rows,cols,group", [(1, 32, 32), (127, 96, 32), (128, 128, 128), (129, 320, 64), (257, 160, 32),
+                                             (384, 1920, 128)])
+def test_recast(dev, in_fmt, fmt, rows, cols, group):
+    g = torch.Generator().manual_seed(rows)
+    check_recast(dev, br.bf16(g, rows, cols, std=2.0), in_fmt, group, fmt)
+
+
+@pytest.mark.parametrize("flags", [ROUND, COL, COL | ROUND, PACKED, PACKED | COL])
+def test_recast_layouts(dev, flags):
+    g = torch.Generator().manual_seed(9)
+    check_recast(dev, br.bf16(g, 500, 224), "e4m3", 32, "e4m3", flags)
+
+
+def test_recast_edges(dev):
+    x = torch.zeros(140, 64, dtype=torch.bfloat16)
+    x[:, 1] = torch.where(torch.arange(140) % 2 == 0, 1e30, -1e30).to(torch.bfloat16)
+    x[3, 2] = 1e-30
+    x[135, 5] = -3.0
+    check_recast(dev, x, "e4m3", 32, "e4m3")
+    check_recast(dev, x, "e5m2", 64, "e5m2", clamp_min=1.0)
+
+
+def test_refusals_of_the_binding(dev):
+    q = torch.zeros(4, 256, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    sf = torch.ones(4, 2, device=dev)
+    dv = torch.zeros(4, 128, dtype=torch.bfloat16, device=dev)
+    ok = pq.qcast_swiglu_backward_checkpoint(q, sf, dv)
+    assert ok.dh.shape == (4, 256) and ok.dh_t.shape == (256, 128) and ok.v_t.shape == (128, 128)
+    for call in (lambda: pq.qcast_swiglu_backward_checkpoint(q, sf, dv.float()),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q.view(torch.uint8), sf, dv),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q, sf[:, :1], dv),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q, sf, dv, fmt="e2m1"),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q, sf, dv, group=64),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q, sf, dv, torch.ones(5, device=dev)),
+                 lambda: pq.qcast_swiglu_backward_checkpoint(q.t(), sf, dv),
+                 lambda: pq.qcast_recast_per_channel_T(q, sf[:3]),
+                 lambda: pq.qcast_recast_per_channel_T(q, torch.ones(4, 3, device=dev)),
+                 lambda: pq.qcast_recast_per_channel_T(q, torch.ones(4, 256, device=dev)),
+                 lambda: pq.qcast_recast_per_channel_T(q, sf.double()),
+                 lambda: pq.qcast_recast_per_channel_T(q, sf, fmt="e5m6"),
+                 lambda: pq.qcast_swiglu_checkpoint(dv, ckpt_fmt="e2m1"),
+                 lambda: pq.qcast_swiglu_checkpoint(dv.float())):
+        with pytest.raises(pq.QcastError):
+            call()
+
+
+def test_empty(dev):
+    q = torch.zeros(0, 256, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    r = pq.qcast_swiglu_backward_checkpoint(q, torch.zeros(0, 2, device=dev),
+                                            torch.zeros(0, 128, dtype=torch.bfloat16, device=dev))
+    assert r.dh.shape == (0, 256) and r.dh_t.shape == (256, 0) and r.dw.shape == (0,)
+    t, tsf = pq.qcast_recast_per_channel_T(q, torch.zeros(0, 2, device=dev))
+    assert t.shape == (256, 0) and tsf.shape == (256, 0)
+    assert pq.qcast_swiglu_checkpoint(torch.zeros(0, 256, dtype=torch.bfloat16, device=dev))[2].shape == (0, 256)

@@ -1,0 +1,250 @@
+"""The norms around a block and their gradient, against the 64-bit formulas
+within the bounds of block_ref, over gates, weights, checkpoints, formats,
+scale layouts, row lengths and counts."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as br
+import oracle
+import precision_quantization_amd as pq
+from precision_quantization_amd import workloads
+
+pytestmark = pytest.mark.gpu
+PACKED, COL, ROUND = pq.SF_PACKED_UE8M0, pq.SF_COL_MAJOR, pq.SF_ROUND_POW2
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.uint8).cpu(), b.view(torch.uint8).cpu())
+
+
+def on(dev, t):
+    return None if t is None else t.to(dev)
+
+
+def d64(t):
+    return None if t is None else t.double()
+
+
+def inputs(rows, cols, kind, post, seed, has_y=True):
+    g = torch.Generator().manual_seed(seed)
+    v = dict(h=br.bf16(g, rows, cols, std=2.0), w_pre=br.bf16(g, cols, std=0.3, mean=1.0), y=None, w_post=None, gate=None)
+    if has_y:
+        v["y"] = br.bf16(g, rows, cols, std=0.7)
+        v["w_post"] = br.bf16(g, cols, std=0.3, mean=1.0) if post else None
+        v["gate"] = br.gate_of(kind, g, rows, cols)
+    v["h"][:, 0] *= 30
+    return v, g
+
+
+def gate64(gate, kind):
+    return None if gate is None else gate.double()
+
+
+def check_forward(dev, rows, cols, kind="channel", post=True, fmt="e4m3", group=128, flags=0, ckpt=None, alpha=0.75,
+                  offset=0.0, has_y=True, want_x=False, want_codes=True, v=None, clamp_min=0.0, eps=1e-6):
+    print(f"norm {rows}x{cols} gate {kind} post {post} {fmt} g{group} flags {flags} ckpt {ckpt}", flush=True)
+    if v is None:
+        v, _ = inputs(rows, cols, kind, post, rows + cols, has_y)
+    alpha = alpha if has_y else 1.0
+    r = pq.qcast_norm_per_token(on(dev, v["h"]), on(dev, v["w_pre"]), on(dev, v["y"]), on(dev, v["w_post"]), on(dev, v["gate"]),
+                                residual_scale=alpha, weight_offset=offset, fmt=fmt, group=group, sf_flags=flags, ckpt_fmt=ckpt,
+                                want_x=want_x, want_codes=want_codes, clamp_min=clamp_min, eps=eps)
+    torch.cuda.synchronize()
+    gate = d64(v["gate"])
+    if kind == "token" and gate is not None:
+        gate = gate[:, None]
+    f = br.norm_forward(d64(v["h"]), d64(v["w_pre"]), d64(v["y"]), d64(v["w_post"]), gate, alpha, offset, eps)
+    # 1/sqrt: half the sum's error and three roundings; h': its own sum's 1/sqrt and five
+    kr = br.U * (br.ROW_SUM / 2 + 4)
+    kh = kr + 6 * br.U
+    if has_y:
+        err = (r.h.cpu().double() - f["h"]).abs()
+        assert (err <= f["h"].abs() * 2.0 ** -8 + (1 + 2.0 ** -8) * kh * f["mag"] + 1e-40).all()
+    else:
+        assert r.h.data_ptr() != 0 and same(r.h, v["h"])
+    # how far h's errors move the second sum: relative to the row's norm
+    moved = (kh * f["mag"]).square().mean(1).sqrt() * f["r2"]
+    assert ((r.rstd_pre.cpu().double() - f["r2"]).abs() <= f["r2"] * (kr + moved) * 1.01).all()
+    if v["w_post"] is not None:
+        assert ((r.rstd_post.cpu().double() - f["r1"]).abs() <= f["r1"] * kr).all()
+    scale = f["r2"][:, None] * (v["w_pre"].double() + offset).abs()
+    slack = scale * (kh * f["mag"] + (kr + moved[:, None] + 4 * br.U) * f["h"].abs())
+    if want_codes:
+        br.check_cast(br.raw(r.out), br.raw(r.out_sf), f["x"], fmt, group, slack.numpy(), flags, clamp_min, "x")
+    else:
+        assert r.out is None
+    if want_x:
+        assert ((r.x.cpu().double() - f["x"]).abs() <= f["x"].abs() * 2.0 ** -8 + slack * 1.01 + 1e-40).all()
+    if ckpt:
+        br.check_cast(br.raw(r.h_ckpt), br.raw(r.h_ckpt_sf), f["h"], ckpt, 128, (kh * f["mag"]).numpy(), 0, 0.0, "h_ckpt")
+        if has_y:
+            q, sf = oracle.per_token(workloads.bf16_bits(v["y"]), ckpt, 128)
+            assert np.array_equal(br.raw(r.y_ckpt), q) and np.array_equal(br.raw(r.y_ckpt_sf), sf)
+    return r, f
+
+
+@pytest.mark.parametrize("kind", [None, "channel", "token", "full"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 1920), (130, 512)])
+def test_forward(dev, kind, post, rows, cols):
+    check_forward(dev, rows, cols, kind, post, ckpt="e4m3", want_x=True)
+
+
+@pytest.mark.parametrize("cols,group", [(32, 32), (160, 32), (64, 64), (2080, 32), (2176, 128), (7168, 128), (8192, 128),
+                                        (8320, 64), (16384, 128), (16416, 32), (32768, 128)])
+def test_forward_row_lengths(dev, cols, group):
+    check_forward(dev, 3, cols, group=group)
+
+
+@pytest.mark.parametrize("fmt,group,flags", [("e5m2", 128, 0), ("e2m1", 32, 0), ("e5m6", 64, 0), ("e4m3", 128, ROUND),
+                                             ("e4m3", 64, COL), ("e2m1", 32, PACKED), ("e4m3", 128, PACKED | COL),
+                                             ("e5m6", 32, COL | ROUND)])
+def test_forward_formats_and_layouts(dev, fmt, group, flags):
+    check_forward(dev, 7, 1536, fmt=fmt, group=group, flags=flags, ckpt="e5m2")
+
+
+def test_forward_first_block_and_last_norm(dev):
+    check_forward(dev, 9, 640, has_y=False, kind=None, ckpt="e4m3")
+    check_forward(dev, 9, 640, kind="token", want_x=True, want_codes=False, offset=1.0)
+    check_forward(dev, 1, 7168, kind=None, alpha=1.0)
+
+
+def test_forward_extreme_rows(dev):
+    v, _ = inputs(6, 256, "channel", True, 4)
+    v["h"][0] = 0
+    v["y"][0] = 0                      # x = 0: zero codes, the floor's scale
+    v["y"][1] = 0                      # the post-norm of a zero row
+    v["h"][2] *= 1e15
+    v["y"][3] *= 1e15                  # squares up to 1e30
+    v["h"][4] *= 1e-10
+    v["y"][4] *= 1e-10                 # far below eps
+    r, _ = check_forward(dev, 6, 256, v=v, ckpt="e4m3")
+    assert not (r.out.view(torch.uint8)[0] & 0x7F).any()
+    check_forward(dev, 6, 256, v=v, clamp_min=0.5)
+
+
+def check_backward(dev, rows, cols, kind="channel", post=True, saved="e4m3", fmt="e4m3", group=128, flags=0, alpha=0.75,
+                   offset=0.0, has_y=True, residual=True, want_dy=False, want_codes=True, seed=0):
+    print(f"norm backward {rows}x{cols} gate {kind} post {post} saved {saved} {fmt} g{group} flags {flags}", flush=True)
+    kind = kind if has_y else None
+    v, g = inputs(rows, cols, kind, post, rows + cols + seed, has_y)
+    dx = br.bf16(g, rows, cols)
+    dh_in = br.bf16(g, rows, cols) if residual else None
+    gate = d64(v["gate"])
+    f = br.norm_forward(d64(v["h"]), d64(v["w_pre"]), d64(v["y"]), d64(v["w_post"]),
+                        gate[:, None] if kind == "token" else gate, alpha, offset)
+    hs, r2 = f["h"].to(torch.bfloat16), f["r2"].float()
+    r1 = None if f["r1"] is None else f["r1"].float()
+    ys, hsf, ysf = v["y"], None, None
+    h64, y64 = hs.double(), d64(ys)
+    if saved != "bf16":
+        hs, hsf, h64 = br.stored(hs, saved)
+        if has_y:
+            ys, ysf, y64 = br.stored(ys, saved)
+    r = pq.qcast_norm_backward_per_token(dx.to(dev), hs.to(dev), r2.to(dev), v["w_pre"].to(dev), dh=on(dev, dh_in),
+                                         saved_h_sf=on(dev, hsf), saved_y=on(dev, ys), saved_y_sf=on(dev, ysf),
+                                         rstd_post=on(dev, r1), w_post=on(dev, v["w_post"]), gate=on(dev, v["gate"]),
+                                         residual_scale=alpha, weight_offset=offset, fmt=fmt, group=group, sf_flags=flags,
+                                         want_dy=want_dy, want_codes=want_codes)
+    torch.cuda.synchronize()
+    args = (d64(dx), d64(dh_in), h64, d64(r2), d64(v["w_pre"]), y64, d64(r1), d64(v["w_post"]), gate, alpha, offset, kind)
+    want, slack = br.norm_backward(*args), br.norm_backward_slack(*args)
+
+    def near(got, name, rounded):
+        err = (got.cpu().double() - want[name]).abs()
+        bound = slack[name] * 1.01 + (want[name].abs() * 2.0 ** -8 if rounded else 0) + 1e-40
+        assert (err <= bound).all(), f"{name}: {(err / bound).max():.3g} of its bound"
+    near(r.dh, "dh", True)
+    near(r.dw_pre, "dw_pre", False)
+    if not has_y:
+        assert r.out is None and r.dy is None and r.dgate is None and r.dw_post is None
+        return r
+    if want_codes:
+        br.check_cast(br.raw(r.out), br.raw(r.out_sf), want["dy"].numpy(), fmt, group, slack["dy"].numpy(), flags, what="dy")
+    if want_dy:
+        near(r.dy, "dy", True)
+    if post:
+        near(r.dw_post, "dw_post", False)
+    if kind:
+        near(r.dgate, "dgate", kind == "full")
+    return r
+
+
+@pytest.mark.parametrize("kind", [None, "channel", "token", "full"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("saved", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (67, 1920)])
+def test_backward(dev, kind, post, saved, rows, cols):
+    check_backward(dev, rows, cols, kind, post, saved, want_dy=True)
+
+
+@pytest.mark.parametrize("rows,cols", [(2, 256), (511, 128), (513, 256), (1100, 384), (3, 7168), (5, 8192), (3, 8320),
+                                       (2, 16384), (3, 16512), (2, 32768)])
+def test_backward_row_counts_and_lengths(dev, rows, cols):
+    check_backward(dev, rows, cols)
+
+
+@pytest.mark.parametrize("cols,group", [(32, 32), (160, 32), (64, 64), (2080, 32)])
+def test_backward_short_groups(dev, cols, group):
+    check_backward(dev, 70, cols, saved="bf16", group=group)
+
+
+@pytest.mark.parametrize("fmt,group,flags", [("e5m2", 128, 0), ("e2m1", 32, 0), ("e5m6", 64, 0), ("e4m3", 128, ROUND),
+                                             ("e4m3", 64, COL), ("e2m1", 32, PACKED), ("e4m3", 128, PACKED | COL)])
+def test_backward_formats_and_layouts(dev, fmt, group, flags):
+    check_backward(dev, 9, 1536, fmt=fmt, group=group, flags=flags)
+
+
+def test_backward_parts(dev):
+    check_backward(dev, 21, 512, has_y=False)
+    check_backward(dev, 21, 512, has_y=False, saved="bf16", residual=False)
+    check_backward(dev, 21, 512, "token", residual=False, offset=1.0)
+    check_backward(dev, 21, 512, "full", want_dy=True, want_codes=False, alpha=1.0)
+
+
+def test_backward_is_deterministic(dev):
+    a, b = (check_backward(dev, 1300, 256, "channel") for _ in range(2))
+    for x, y in zip(a, b):
+        assert x is None or same(x, y)
+
+
+def test_backward_of_no_rows_gives_zero_weight_gradients(dev):
+    e = torch.zeros(0, 256, dtype=torch.bfloat16, device=dev)
+    w = torch.ones(256, dtype=torch.bfloat16, device=dev)
+    r = pq.qcast_norm_backward_per_token(e, e, torch.zeros(0, device=dev), w, saved_y=e, rstd_post=torch.zeros(0, device=dev),
+                                         w_post=w, gate=w)
+    for t in (r.dw_pre, r.dw_post, r.dgate):
+        assert t.shape == (256,) and not t.any()
+    f = pq.qcast_norm_per_token(e, w, e, w, ckpt_fmt="e4m3")
+    assert f.out.shape == (0, 256) and f.h_ckpt_sf.shape == (0, 2)
+
+
+def test_refusals_of_the_binding(dev):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=dev)
+    w = torch.ones(256, dtype=torch.bfloat16, device=dev)
+    r = torch.ones(4, device=dev)
+    q = x.to(torch.float8_e4m3fn)
+    sf = torch.ones(4, 2, device=dev)
+    bad_norm = [dict(y=None, w_post=w), dict(gate=torch.ones(5, device=dev)), dict(gate=torch.ones(4, 1, device=dev)),
+                dict(gate=w[:128]), dict(w_post=w.float()), dict(ckpt_fmt="e5m6"), dict(want_codes=False), dict(group=96),
+                dict(eps=-1.0), dict(residual_scale=float("nan")), dict(y=x[:, :128]), dict(y=None, residual_scale=0.5)]
+    for kw in bad_norm:
+        with pytest.raises(pq.QcastError):
+            pq.qcast_norm_per_token(x, w, **{"y": x, **kw})
+    bad_back = [dict(w_post=w), dict(rstd_post=r), dict(saved_y=None, gate=w), dict(saved_y_sf=sf), dict(dh=x.float()),
+                dict(want_codes=False), dict(group=96)]
+    for kw in bad_back:
+        with pytest.raises(pq.QcastError):
+            pq.qcast_norm_backward_per_token(x, x, r, w, **{"saved_y": x, **kw})
+    for kw in (dict(saved_h_sf=None), dict(saved_h_sf=sf[:, :1]), dict(saved_h_sf=sf, saved_y=x),
+               dict(saved_h_sf=sf, saved_y=q), dict(saved_h_sf=sf, saved_y=x.to(torch.float8_e5m2), saved_y_sf=sf)):
+        with pytest.raises(pq.QcastError):
+            pq.qcast_norm_backward_per_token(x, q, r, w, **kw)

@@ -552,9 +552,9 @@ QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, i
  *            least one of q (with sf) and dy_out is given.
  *   dw_pre, dw_post  [cols] fp32; dgate [cols] fp32, [rows] fp32 or [rows,
  *            cols] bf16 by gate_kind. Each may be NULL; all are overwritten.
- *   ws       min(rows, QCAST_NORM_WS_ROWS) * 3 * cols * 4 bytes of device
+ *   ws       min(rows, QCAST_NORM_WS_ROWS) * 2 * cols * 4 bytes of device
  *            memory (16-byte aligned; no particular contents) that no other
- *            call uses at the same time; may be NULL when rows <= 1.
+ *            call uses at the same time; may be NULL when rows is 0.
  *   Everything else as qcast_norm_per_token.
  */
 QCAST_API int qcast_norm_backward_per_token(

@@ -809,8 +809,8 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
             dw_post = torch.empty(cols, dtype=f32, device=dev)
         if kind:
             dgate = torch.empty(gate.shape, dtype=bf16 if kind == GATE_FULL else f32, device=dev)
-        if rows > 1:
-            ws = torch.empty(min(rows, NORM_WS_ROWS) * 3 * cols, dtype=f32, device=dev)
+        if rows:
+            ws = torch.empty(min(rows, NORM_WS_ROWS) * 2 * cols, dtype=f32, device=dev)
         check(load().qcast_norm_backward_per_token(
             dx.data_ptr(), dhptr, rows, cols, sf, shptr, shsf, syptr, sysf, r1ptr, r2ptr, wpptr,
             wqptr, gptr, kind, residual_scale, weight_offset, f, group, clamp_min, sf_flags,

@@ -21,10 +21,15 @@
 //   sum da * a = S2 - r2 * (S1 / n) * S3.
 //
 // gfx950 design. Workgroups walk the rows with a stride, so a lane meets the
-// same columns in every row and holds the sums of both weights' gradients and
-// of a channel gate's in fp32 registers; each workgroup writes its sums to
-// the workspace once and a second kernel adds them up in a fixed order (no
-// atomics: the result does not depend on which workgroup ends first).
+// same columns in every row and holds the column sums in fp32 registers; each
+// workgroup writes its sums to the workspace once and a second kernel adds
+// them up in a fixed order (no atomics, and a grid that follows from the
+// sizes alone: the result depends on nothing else). A channel gate and w_post
+// are the same in every row, so their gradients are one sum T = sum d * a:
+// dw_post = gate * T, dgate = wp * T. With one chunk of 8 columns per lane
+// (rows of up to 8192) the next row is loaded while the current one is
+// worked on, and the values of the first half are kept for the second; longer
+// rows keep the packed inputs and form the values again.
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -33,254 +38,301 @@ namespace qcast {
 namespace {
 
 constexpr int kMaxWaves = 16;
-constexpr int kJoinRows = 16;      // waves of the joining workgroup
+constexpr int kJoinWaves = 16;     // waves of the joining workgroup
 
-// The lane's raw data of one chunk of one row.
-template <bool kSaved8>
+// The lane's raw data of one chunk of one row: bf16 octets, or 8-bit codes in
+// the low two words with their scales.
+// r1, r2 and a token gate of its row travel with it, so that nothing loaded
+// later has to be waited for before the row can be worked on.
 struct Chunk {
-  u32x4 dx, dh, gate;
-  u32x4 hs, ys;          // kSaved8: the codes in the low half
-  float hsf, ysf;
+  u32x4 dx, dh, gate, hs, ys;
+  float hsf, ysf, r1, r2, row_gate;
 };
 
-template <bool kSaved8>
-__device__ __forceinline__ Chunk<kSaved8> load_chunk(const NormBackward& p, uint32_t row,
-                                                     uint32_t jc, bool valid) {
+template <int kSaved, int kGate, bool kY>
+__device__ __forceinline__ Chunk load_chunk(const NormBackward& p, uint32_t row, uint32_t jc,
+                                            bool valid) {
   const int64_t at = (int64_t)row * p.chunks + jc;
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  Chunk<kSaved8> c;
-  c.dx = valid ? load_stream(reinterpret_cast<const u32x4*>(p.dx) + at) : zero;
-  c.dh = (valid && p.dh_in) ? load_stream(reinterpret_cast<const u32x4*>(p.dh_in) + at) : zero;
-  c.gate = (valid && p.gate_kind == kGateFull)
-               ? load_stream(reinterpret_cast<const u32x4*>(p.gate) + at)
-               : zero;
-  c.hs = zero;
-  c.ys = zero;
-  c.hsf = c.ysf = 1.0f;
-  if constexpr (kSaved8) {
-    if (valid) {
-      const u32x2 h = load_stream(static_cast<const u32x2*>(p.saved_h) + at);
-      c.hs.x = h.x;
-      c.hs.y = h.y;
-      const int64_t s = (int64_t)row * (p.chunks / 16) + jc / 16;
-      c.hsf = p.saved_h_sf[s];
-      if (p.saved_y) {
-        const u32x2 y = load_stream(static_cast<const u32x2*>(p.saved_y) + at);
-        c.ys.x = y.x;
-        c.ys.y = y.y;
-        c.ysf = p.saved_y_sf[s];
-      }
+  Chunk c;
+  c.dx = c.dh = c.gate = c.hs = c.ys = zero;
+  c.hsf = c.ysf = c.r1 = c.row_gate = 1.0f;
+  c.r2 = p.rstd_pre[row];
+  if (kY && p.rstd_post) c.r1 = p.rstd_post[row];
+  if (kGate == kGateToken) c.row_gate = static_cast<const float*>(p.gate)[row];
+  if (!valid) return c;
+  c.dx = load_stream(reinterpret_cast<const u32x4*>(p.dx) + at);
+  if (p.dh_in) c.dh = load_stream(reinterpret_cast<const u32x4*>(p.dh_in) + at);
+  if (kGate == kGateFull) c.gate = load_stream(reinterpret_cast<const u32x4*>(p.gate) + at);
+  if constexpr (kSaved != 0) {
+    const int64_t s = (int64_t)row * (p.chunks / 16) + jc / 16;
+    const u32x2 h = load_stream(static_cast<const u32x2*>(p.saved_h) + at);
+    c.hs.x = h.x;
+    c.hs.y = h.y;
+    c.hsf = p.saved_h_sf[s];
+    if (kY) {
+      const u32x2 y = load_stream(static_cast<const u32x2*>(p.saved_y) + at);
+      c.ys.x = y.x;
+      c.ys.y = y.y;
+      c.ysf = p.saved_y_sf[s];
     }
   } else {
-    if (valid) {
-      c.hs = load_stream(static_cast<const u32x4*>(p.saved_h) + at);
-      if (p.saved_y) c.ys = load_stream(static_cast<const u32x4*>(p.saved_y) + at);
-    }
+    c.hs = load_stream(static_cast<const u32x4*>(p.saved_h) + at);
+    if (kY) c.ys = load_stream(static_cast<const u32x4*>(p.saved_y) + at);
   }
   return c;
 }
 
-template <bool kSaved8>
-__device__ __forceinline__ void saved_values(const u32x4& raw, float sf, int fmt, float v[8]) {
-  if constexpr (kSaved8) {
-    const u32x2 w = {raw.x, raw.y};
-    if (fmt == kE4M3) decode8<kE4M3>(w, sf, v);
-    else decode8<kE5M2>(w, sf, v);
+template <int kSaved>
+__device__ __forceinline__ void saved_values(const u32x4& raw, float sf, float v[8]) {
+  if constexpr (kSaved != 0) {
+    decode8<kSaved>(u32x2{raw.x, raw.y}, sf, v);
   } else {
     unpack8(raw, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * sf;
   }
 }
 
-template <int kC, bool kSaved8>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uint32_t rows) {
-  __shared__ float part[2][kMaxWaves][3];
-  const uint32_t chunks = p.chunks;
-  const int waves = blockDim.x >> 6;
+// The factors of a chunk's columns: q = w_pre + offset, and c = wp (times a
+// channel gate; 1 without w_post).
+__device__ __forceinline__ void column_factors(const NormBackward& p, uint32_t jc, bool valid,
+                                               float q[8], float c[8]) {
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  u32x4 wq[kC], wp[kC], gc[kC];
-  float s_pre[kC][8], s_post[kC][8], s_gate[kC][8];
+  unpack8(valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero, q);
+  unpack8((valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero, c);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = q[i] + p.offset;
+    c[i] = p.w_post ? c[i] + p.offset : 1.0f;
+  }
+  if (p.gate_kind == kGateChannel) {
+    float g[8];
+    unpack8(valid ? reinterpret_cast<const u32x4*>(p.gate)[jc] : zero, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = c[i] * g[i];
+  }
+}
+
+// The fp32 values of a chunk that both halves of a row's work use.
+struct Values {
+  float x[8], a[8], gx[8], dh[8], c[8];   // xh, a, dx * q, dh', gate * wp
+};
+
+template <int kSaved, int kGate, bool kY>
+__device__ __forceinline__ Values chunk_values(const Chunk& ch, const float q[8],
+                                               const float c[8], float dx[8]) {
+  Values v;
+  unpack8(ch.dx, dx);
+  unpack8(ch.dh, v.dh);
+  // code * sf * r in one product: code * (sf * r)
+  saved_values<kSaved>(ch.hs, kSaved ? ch.hsf * ch.r2 : ch.r2, v.x);
+  if (kY) saved_values<kSaved>(ch.ys, kSaved ? ch.ysf * ch.r1 : ch.r1, v.a);
+  float g[8];
+  if (kGate == kGateFull) unpack8(ch.gate, g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v.gx[i] = dx[i] * q[i];
+    v.c[i] = kGate == kGateFull ? c[i] * g[i] : c[i];
+  }
+  return v;
+}
+
+// kSaved: 0 for bf16, else the format of the 8-bit checkpoints. kGate:
+// kGateFull, kGateToken, or kGateNone for both other kinds (a channel gate is
+// one of the column factors). kY: there is a block output.
+template <int kC, int kSaved, int kGate, bool kY>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uint32_t rows) {
+  constexpr bool kKeep = kC == 1;
+  __shared__ __attribute__((aligned(16))) float part[2][kMaxWaves][4];
+  const uint32_t chunks = p.chunks;
+  constexpr bool kFull = kGate == kGateFull;
+  float q[kC][8], c[kC][8], s_pre[kC][8], s_post[kC][8];
 #pragma unroll
   for (int k = 0; k < kC; ++k) {
     const uint32_t jc = threadIdx.x + k * blockDim.x;
-    const bool valid = jc < chunks;
-    wq[k] = valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero;
-    wp[k] = (valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero;
-    gc[k] = (valid && p.gate_kind == kGateChannel) ? reinterpret_cast<const u32x4*>(p.gate)[jc]
-                                                   : zero;
+    if (kKeep) column_factors(p, jc, jc < chunks, q[k], c[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[k][i] = s_post[k][i] = s_gate[k][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) s_pre[k][i] = s_post[k][i] = 0.0f;
   }
-  const bool has_gate_vec = p.gate_kind == kGateChannel || p.gate_kind == kGateFull;
+  Chunk next;
+  if (kKeep)
+    next = load_chunk<kSaved, kGate, kY>(p, blockIdx.x, threadIdx.x, threadIdx.x < chunks);
   int parity = 0;
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
-    Chunk<kSaved8> c[kC];
+    Chunk ch[kC];
+    if constexpr (kKeep) {
+      ch[0] = next;
+      if (row + gridDim.x < rows)
+        next = load_chunk<kSaved, kGate, kY>(p, row + gridDim.x, threadIdx.x,
+                                             threadIdx.x < chunks);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        const uint32_t jc = threadIdx.x + k * blockDim.x;
+        ch[k] = load_chunk<kSaved, kGate, kY>(p, row, jc, jc < chunks);
+      }
+    }
+    const float r1 = ch[0].r1, r2 = ch[0].r2, row_gate = ch[0].row_gate;
+    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    Values kept;
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
-      c[k] = load_chunk<kSaved8>(p, row, jc, jc < chunks);
-    }
-    const float r2 = p.rstd_pre[row];
-    const float r1 = p.rstd_post ? p.rstd_post[row] : 1.0f;
-    const float row_gate =
-        p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
-    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kC; ++k) {
-      float dx[8], dh[8], xh[8], a[8], q[8], w[8], g[8];
-      unpack8(c[k].dx, dx);
-      unpack8(c[k].dh, dh);
-      saved_values<kSaved8>(c[k].hs, c[k].hsf, p.saved_fmt, xh);
-      saved_values<kSaved8>(c[k].ys, c[k].ysf, p.saved_fmt, a);
-      unpack8(wq[k], q);
-      unpack8(wp[k], w);
-      unpack8(p.gate_kind == kGateFull ? c[k].gate : gc[k], g);
+      if (!kKeep) column_factors(p, jc, jc < chunks, q[k], c[k]);
+      float dx[8];
+      const Values v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x = xh[i] * r2;
-        const float gx = dx[i] * (q[i] + p.offset);
-        s1 = __builtin_fmaf(gx, x, s1);
-        s_pre[k][i] = __builtin_fmaf(dx[i], x, s_pre[k][i]);
-        if (p.saved_y) {
-          float cc = a[i] * r1;
-          if (p.w_post) cc = cc * (w[i] + p.offset);
-          if (has_gate_vec) cc = cc * g[i];
-          s2 = __builtin_fmaf(__builtin_fmaf(r2, gx, dh[i]), cc, s2);
-          s3 = __builtin_fmaf(x, cc, s3);
+        s1 = __builtin_fmaf(v.gx[i], v.x[i], s1);
+        s_pre[k][i] = __builtin_fmaf(dx[i], v.x[i], s_pre[k][i]);
+        if (kY) {
+          const float cc = v.a[i] * v.c[i];
+          s2 = __builtin_fmaf(__builtin_fmaf(r2, v.gx[i], v.dh[i]), cc, s2);
+          s3 = __builtin_fmaf(v.x[i], cc, s3);
         }
       }
+      if (kKeep) kept = v;
     }
-    s1 = wave_sum(s1);
-    if (p.saved_y) {
-      s2 = wave_sum(s2);
-      s3 = wave_sum(s3);
-    }
-    if (waves > 1) {
-      if ((threadIdx.x & 63) == 0) {
-        float* o = part[parity][threadIdx.x >> 6];
-        o[0] = s1;
-        o[1] = s2;
-        o[2] = s3;
-      }
-      __syncthreads();
-      s1 = s2 = s3 = 0.0f;
-      for (int i = 0; i < waves; ++i) {
-        s1 += part[parity][i][0];
-        s2 += part[parity][i][1];
-        s3 += part[parity][i][2];
-      }
-    }
-    const float m1 = s1 / p.n;
-    const float along = s2 - r2 * m1 * s3;      // sum dH * c, without a token gate
-    if (p.gate_kind == kGateToken && p.dgate && threadIdx.x == 0)
+    block_sum3(s1, s2, s3, part[parity]);
+    const float m1 = s1 * p.inv_n;
+    const float along = s2 - r2 * m1 * s3;      // sum dH * a * c, without a token gate
+    if (kY && kGate == kGateToken && p.dgate && threadIdx.x == 0)
       static_cast<float*>(p.dgate)[row] = along;
-    const float m2 = p.w_post ? along * row_gate / p.n : 0.0f;
+    const float m2 = (kY && p.w_post) ? along * row_gate * p.inv_n : 0.0f;
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
-      float dx[8], dh[8], xh[8], a[8], q[8], w[8], g[8], dgate[8], dy[8];
-      unpack8(c[k].dx, dx);
-      unpack8(c[k].dh, dh);
-      saved_values<kSaved8>(c[k].hs, c[k].hsf, p.saved_fmt, xh);
-      saved_values<kSaved8>(c[k].ys, c[k].ysf, p.saved_fmt, a);
-      unpack8(wq[k], q);
-      unpack8(wp[k], w);
-      unpack8(p.gate_kind == kGateFull ? c[k].gate : gc[k], g);
+      Values v;
+      if constexpr (kKeep) {
+        v = kept;
+      } else {
+        float dx[8];
+        column_factors(p, jc, jc < chunks, q[k], c[k]);
+        v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx);
+      }
+      float g[8], d[8], out[8];
+      if (kFull) unpack8(ch[k].gate, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float gx = dx[i] * (q[i] + p.offset);
-        const float d = __builtin_fmaf(r2, gx - xh[i] * r2 * m1, dh[i]);
-        dh[i] = p.alpha * d;
-        const float aa = a[i] * r1;
-        const float wi = p.w_post ? w[i] + p.offset : 1.0f;
-        dgate[i] = d * aa * wi;
-        const float dz = (has_gate_vec ? d * g[i] : d) * row_gate;
-        s_post[k][i] = __builtin_fmaf(dz, aa, s_post[k][i]);
-        if (p.gate_kind == kGateChannel) s_gate[k][i] += dgate[i];
-        dy[i] = p.w_post ? r1 * (dz * wi - aa * m2) : dz;
+        d[i] = __builtin_fmaf(r2, __builtin_fmaf(-v.x[i], m1, v.gx[i]), v.dh[i]);
+        out[i] = p.alpha * d[i];
       }
-      if (jc < chunks) {
-        const int64_t at = (int64_t)row * chunks + jc;
-        store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, pack8_bf16(dh));
-        if (p.saved_y) {
-          if (p.gate_kind == kGateFull && p.dgate)
-            store_stream(static_cast<u32x4*>(p.dgate) + at, pack8_bf16(dgate));
-          if (p.dy_out) store_stream(reinterpret_cast<u32x4*>(p.dy_out) + at, pack8_bf16(dy));
-          if (p.cast.q) cast_chunk(p.cast, row, jc, chunks, dy);
+      const int64_t at = (int64_t)row * chunks + jc;
+      if (jc < chunks)
+        store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, pack8_bf16(out));
+      if (kY) {
+        // without the column's own factors: d * a * (token or elementwise gate)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float dz = kFull ? d[i] * g[i] : kGate == kGateToken ? d[i] * row_gate : d[i];
+          s_post[k][i] = __builtin_fmaf(dz, v.a[i], s_post[k][i]);
+          out[i] = dz * (kFull ? c[k][i] : v.c[i]);
+          if (p.w_post) out[i] = r1 * __builtin_fmaf(-v.a[i], m2, out[i]);
+        }
+        if (jc < chunks) {
+          if (kFull && p.dgate) {
+            float dg[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dg[i] = d[i] * v.a[i] * c[k][i];
+            store_stream(static_cast<u32x4*>(p.dgate) + at, pack8_bf16(dg));
+          }
+          if (p.dy_out) store_stream(reinterpret_cast<u32x4*>(p.dy_out) + at, pack8_bf16(out));
+          if (p.cast.q) cast_chunk(p.cast, row, jc, chunks, out);
         }
       }
     }
   }
-  // this workgroup's column sums: [workgroup][vector][column]
+  // this workgroup's column sums: [workgroup][2][column]
 #pragma unroll
   for (int k = 0; k < kC; ++k) {
     const uint32_t jc = threadIdx.x + k * blockDim.x;
     if (jc < chunks) {
+      float* o = p.ws + (int64_t)blockIdx.x * 2 * 8 * chunks + 8 * jc;
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-      for (int v = 0; v < 3; ++v) {
-        float* const to = p.sums[v];
-        if (!to) continue;
-        float* o = gridDim.x == 1 ? to + 8 * jc
-                                  : p.ws + ((int64_t)blockIdx.x * 3 + v) * 8 * chunks + 8 * jc;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = v == 0 ? s_pre[k][i] : v == 1 ? s_post[k][i] : s_gate[k][i];
+      for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<f32x4*>(o + i) =
+            f32x4{s_pre[k][i], s_pre[k][i + 1], s_pre[k][i + 2], s_pre[k][i + 3]};
+        if (kY)
+          *reinterpret_cast<f32x4*>(o + 8 * chunks + i) =
+              f32x4{s_post[k][i], s_post[k][i + 1], s_post[k][i + 2], s_post[k][i + 3]};
       }
     }
   }
 }
 
-// out[v][col] = sum over the `parts` workgroups of ws[part][v][col], in a
-// fixed order: wave w of a workgroup adds parts w, w + 16, ..., then the 16
-// partial sums are added in order.
-__global__ __launch_bounds__(64 * kJoinRows) void norm_backward_join_kernel(
-    const float* __restrict__ ws, uint32_t parts, uint32_t cols, NormSums out) {
-  __shared__ float part[kJoinRows][64];
+// The column gradients from the sums of `parts` workgroups, added in a fixed
+// order: wave w of a workgroup adds parts w, w + 16, ..., then the 16 partial
+// sums are added in order. blockIdx.y 0: dw_pre; 1: T, which gives dw_post
+// (times a channel gate) and a channel gate's gradient (times wp).
+__global__ __launch_bounds__(64 * kJoinWaves) void norm_backward_join_kernel(NormBackward p,
+                                                                           uint32_t parts) {
+  __shared__ float part[kJoinWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
+  const uint32_t cols = p.chunks * 8;
   const uint32_t col = blockIdx.x * 64 + lane;
-  const int v = blockIdx.y;
-  float* const to = out.p[v];
-  if (!to) return;                       // uniform over the workgroup
+  const float* ws = p.ws + (int64_t)blockIdx.y * cols + col;
   float s = 0.0f;
-  if (col < cols)
-    for (uint32_t i = wave; i < parts; i += kJoinRows) s += ws[((int64_t)i * 3 + v) * cols + col];
+  if (col < cols) {
+#pragma unroll 8
+    for (uint32_t i = wave; i < parts; i += kJoinWaves) s += ws[(int64_t)i * 2 * cols];
+  }
   part[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < cols) {
-    float t = part[0][lane];
-    for (int i = 1; i < kJoinRows; ++i) t += part[i][lane];
-    to[col] = t;
+  if (wave != 0 || col >= cols) return;
+  float t = part[0][lane];
+  for (int i = 1; i < kJoinWaves; ++i) t += part[i][lane];
+  if (blockIdx.y == 0) {
+    if (p.sums[0]) p.sums[0][col] = t;
+    return;
   }
+  const bool channel = p.gate_kind == kGateChannel;
+  if (p.sums[1])
+    p.sums[1][col] =
+        channel ? t * bf16_lo(static_cast<const uint16_t*>(p.gate)[col]) : t;
+  if (p.sums[2]) p.sums[2][col] = p.w_post ? t * (bf16_lo(p.w_post[col]) + p.offset) : t;
+}
+
+template <int kC, int kSaved>
+auto pick(const NormBackward& p) {
+  return !p.saved_y                    ? norm_backward_kernel<kC, kSaved, kGateNone, false>
+         : p.gate_kind == kGateFull  ? norm_backward_kernel<kC, kSaved, kGateFull, true>
+         : p.gate_kind == kGateToken ? norm_backward_kernel<kC, kSaved, kGateToken, true>
+                                     : norm_backward_kernel<kC, kSaved, kGateNone, true>;
+}
+template <int kC>
+auto pick_saved(const NormBackward& p) {
+  return p.saved_fmt == 0       ? pick<kC, 0>(p)
+         : p.saved_fmt == kE4M3 ? pick<kC, kE4M3>(p)
+                                : pick<kC, kE5M2>(p);
 }
 
 }  // namespace
 
+// Workgroups of the pass: one per row up to kNormParts.
+uint32_t norm_backward_parts(int64_t rows) {
+  return (uint32_t)(rows < kNormParts ? rows : kNormParts);
+}
+
 hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, hipStream_t stream) {
   if (p.chunks == 0) return hipSuccess;
-  const uint32_t cols = p.chunks * 8;
-  const NormSums out{{p.sums[0], p.sums[1], p.sums[2]}};
-  const bool any_sum = out.p[0] || out.p[1] || out.p[2];
-  if (rows == 0) {                       // sums over no rows: zeros
-    if (!any_sum) return hipSuccess;
-    launch_kernel(norm_backward_join_kernel, dim3((cols + 63) / 64, 3), dim3(64 * kJoinRows), 0,
-                  stream, (const float*)nullptr, 0u, cols, out);
-    return hipGetLastError();
-  }
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
-  const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
-  const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
-  const unsigned grid = (unsigned)(rows < kNormParts ? rows : kNormParts);
-  auto kernel = p.saved_fmt ? (kc == 1   ? norm_backward_kernel<1, true>
-                               : kc == 2 ? norm_backward_kernel<2, true>
-                                         : norm_backward_kernel<4, true>)
-                            : (kc == 1   ? norm_backward_kernel<1, false>
-                               : kc == 2 ? norm_backward_kernel<2, false>
-                                         : norm_backward_kernel<4, false>);
-  launch_kernel(kernel, dim3(grid), dim3(threads), 0, stream, p, (uint32_t)rows);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess || grid == 1 || !any_sum) return err;
-  launch_kernel(norm_backward_join_kernel, dim3((cols + 63) / 64, 3), dim3(64 * kJoinRows), 0,
-                stream, (const float*)p.ws, (uint32_t)grid, cols, out);
+  const uint32_t parts = norm_backward_parts(rows);
+  if (parts) {
+    const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
+    const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
+    auto kernel = kc == 1 ? pick_saved<1>(p) : kc == 2 ? pick_saved<2>(p) : pick_saved<4>(p);
+    launch_kernel(kernel, dim3(parts), dim3(threads), 0, stream, p, (uint32_t)rows);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  // with no rows, the sums over them: zeros
+  if (!p.sums[0] && !p.sums[1] && !p.sums[2]) return hipSuccess;
+  launch_kernel(norm_backward_join_kernel,
+                dim3((p.chunks * 8 + 63) / 64, p.sums[1] || p.sums[2] ? 2 : 1),
+                dim3(64 * kJoinWaves), 0, stream, p, parts);
   return hipGetLastError();
 }
 

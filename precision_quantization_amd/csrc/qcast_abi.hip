@@ -166,7 +166,7 @@ int device_ok() {
 }
 
 static_assert(QCAST_NORM_MAX_COLS == 8 * qcast::kNormMaxChunks, "longest row of the norms");
-static_assert(QCAST_NORM_WS_ROWS == qcast::kNormParts, "workspace rows of the norms");
+static_assert(QCAST_NORM_WS_ROWS >= qcast::kNormParts, "workspace rows of the norms");
 
 // The scalar arguments of the norm entry points; `saved_fmt` is the format
 // of 8-bit checkpoints, 0 for none.
@@ -644,7 +644,7 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
         (saved_y_sf != nullptr)) || (rstd_post != nullptr) != (w_post != nullptr) ||
         (gate != nullptr) != (gate_kind != QCAST_GATE_NONE) ||
         (q != nullptr) != (sf != nullptr) || (saved_y && !q && !dy_out) ||
-        (!saved_y && (w_post || gate || q || dy_out)) || (rows > 1 && !ws))
+        (!saved_y && (w_post || gate || q || dy_out)) || !ws)
       return QCAST_ERR_NULL;
   }
   if ((dw_post && !w_post) || (dgate && !gate)) return QCAST_ERR_NULL;
@@ -684,7 +684,7 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
   p.gate_kind = gate_kind;
   p.alpha = residual_scale;
   p.offset = weight_offset;
-  p.n = (float)cols;
+  p.inv_n = 1.0f / (float)cols;
   p.chunks = (uint32_t)(cols / 8);
   return finish(qcast::launch_norm_backward(p, rows, static_cast<hipStream_t>(stream)));
 }

@@ -184,7 +184,10 @@ bool tile_fits(int64_t rows, int64_t cols, int64_t stride);
 // The norms around a block (norm.hip, norm_backward.hip).
 enum GateKind : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
 constexpr uint32_t kNormMaxChunks = 4096;      // 32768 columns: 1024 threads x 4 chunks of 8
-constexpr int64_t kNormParts = 512;            // workgroups of the backward pass
+#ifndef QCAST_NB_PARTS
+#define QCAST_NB_PARTS 256
+#endif
+constexpr int64_t kNormParts = QCAST_NB_PARTS;
 
 struct NormForward {
   const uint16_t* y;         // or null
@@ -204,9 +207,6 @@ struct NormForward {
 };
 hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream);
 
-struct NormSums {
-  float* p[3];               // [cols] each, or null
-};
 struct NormBackward {
   const uint16_t* dx;
   const uint16_t* dh_in;     // or null
@@ -223,12 +223,12 @@ struct NormBackward {
   uint16_t* dy_out;          // or null
   float* sums[3];            // dw_pre, dw_post, dgate of a channel gate; each may be null
   void* dgate;               // of a token or full gate, or null
-  float* ws;                 // [min(rows, kNormParts)][3][cols]
+  float* ws;                 // [min(rows, kNormParts)][2][cols]
   RowCast cast;
   int saved_fmt;             // 0: bf16
   int gate_kind;
   float alpha, offset;
-  float n;
+  float inv_n;               // 1 / cols
   uint32_t chunks;
 };
 hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, hipStream_t stream);

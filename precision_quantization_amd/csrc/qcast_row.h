@@ -34,6 +34,28 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float((uint32_t)s[0]) + __uint_as_float((uint32_t)s[1]);
 }
 
+// Sums of three values over the workgroup (at most 16 waves), the same bits
+// in every thread: `part` holds one row of 4 words per wave. One barrier;
+// every lane then reads one wave's row (one LDS trip, however many waves) and
+// the rows are added across the 16 lanes.
+__device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float (*part)[4]) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  c = wave_sum(c);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  if ((threadIdx.x & 63) == 0)
+    *reinterpret_cast<f32x4*>(part[threadIdx.x >> 6]) = f32x4{a, b, c, 0.0f};
+  __syncthreads();
+  const int i = threadIdx.x & 15;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (i < waves) v = *reinterpret_cast<const f32x4*>(part[i]);
+  a = row16_sum(v.x);
+  b = row16_sum(v.y);
+  c = row16_sum(v.z);
+}
+
 // Abs-max over the aligned run of 2^shift lanes (4, 8 or 16; shift is the
 // same in every lane).
 __device__ __forceinline__ float run_max(float m, int shift) {

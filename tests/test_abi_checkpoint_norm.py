@@ -166,7 +166,7 @@ def test_norm_backward(lib):
     if not gpu_available():
         # sums over no rows are zeros, which a kernel has to write
         assert nbwd(lib, rows=0, dx=None) == ERR_DEVICE
-        assert nbwd(lib, rows=1, ws=None) == ERR_DEVICE
+        assert nbwd(lib, rows=1) == ERR_DEVICE
 
 
 def test_binding_refuses_cpu_tensors():

@@ -3,10 +3,11 @@
 // transposed, and the scales of the 128 channels.
 //
 // Codes wait in LDS as rows of 128 tokens (32 dwords) per channel, a dword
-// holding 4 consecutive tokens. The dword index is XOR-swizzled in whole
-// 16-byte groups by the channel, so that lanes writing the same tokens of
-// different channels spread over the banks and a 16-byte run of tokens stays
-// contiguous for the read-back.
+// holding 4 consecutive tokens. Rows are 36 dwords apart and the dword index
+// is XOR-swizzled in whole 16-byte groups by the channel: 16 lanes writing
+// channels 8 (or 16) apart and the same tokens then fall on distinct banks
+// (36 * 8 is 32 mod 64, so every other such lane takes the other half), and a
+// 16-byte run of tokens stays contiguous and aligned for the read-back.
 #pragma once
 
 #include "qcast_device.h"
@@ -31,18 +32,24 @@ inline TileWalk make_tile_walk(int64_t rows, int64_t cols) {
   return w;
 }
 
+constexpr uint32_t kTileRowDw = 36;
+constexpr uint32_t kTileDw = kTile * kTileRowDw;
 __device__ __forceinline__ uint32_t swizzled(uint32_t channel, uint32_t dword) {
-  return channel * 32 + (dword ^ (4 * ((channel >> 3) & 7)));
+  return channel * kTileRowDw + (dword ^ (4 * ((channel >> 4) & 7)));
 }
 
 // The scale of one channel over the tile's tokens, formed and stored by one
 // lane; returns what its values are multiplied by.
-template <int kFmt>
-__device__ __forceinline__ float channel_scale(const TileCast& out, uint32_t channel,
+template <int kFmt, bool kLayout>
+__device__ __forceinline__ float channel_scale(void* sf, const SfLayout& lay, uint32_t channel,
                                                uint32_t group, float amax, float floor) {
   Scale s = group_scale<kFmt>(amax, floor);
-  if (out.lay.flags & kSfRound) s = round_scale_pow2(s);
-  store_lone_scale(out.sf, channel, group, s, out.lay);
+  if (kLayout) {
+    if (lay.flags & kSfRound) s = round_scale_pow2(s);
+    store_lone_scale(sf, channel, group, s, lay);
+  } else {
+    static_cast<float*>(sf)[(uint64_t)channel * lay.gpr + group] = s.sf;
+  }
   return s.inv;
 }
 

@@ -29,9 +29,9 @@ __device__ __forceinline__ void decode_word(uint32_t w, float sf, float v[4]) {
   for (int i = 0; i < 4; ++i) v[i] = v[i] * sf;
 }
 
-template <int kIn, int kFmt>
+template <int kIn, int kFmt, bool kLayout>
 __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk tw) {
-  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * 32];
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTileDw];
   __shared__ float amax_s[kThreads / 64][kTile];
   __shared__ float inv_s[kTile];
   const uint32_t tau = (blockIdx.x % kTileXcds) * tw.per_xcd + blockIdx.x / kTileXcds;
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk
     float m = amax_s[0][c];
 #pragma unroll
     for (int i = 1; i < kThreads / 64; ++i) m = fmaxf(m, amax_s[i][c]);
-    if (c < nc) inv_s[c] = channel_scale<kFmt>(p.out, c0 + c, gt, m, p.floor);
+    if (c < nc) inv_s[c] = channel_scale<kFmt, kLayout>(p.out.sf, p.out.lay, c0 + c, gt, m, p.floor);
   }
   __syncthreads();
   if (valid_ch) {
@@ -106,6 +106,12 @@ __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk
   store_tile_rows<kThreads>(tile, p.out.qT, c0, nc, gt, tw.ntg * kTile);
 }
 
+// kLayout: scale options other than plain fp32.
+template <int kIn, int kFmt>
+auto pick(bool layout) {
+  return layout ? recast_kernel<kIn, kFmt, true> : recast_kernel<kIn, kFmt, false>;
+}
+
 }  // namespace
 
 bool tile_fits(int64_t rows, int64_t cols, int64_t stride) {
@@ -120,9 +126,9 @@ bool tile_fits(int64_t rows, int64_t cols, int64_t stride) {
 hipError_t launch_recast(const RecastTile& p, int in_fmt, int fmt, hipStream_t stream) {
   const TileWalk tw = make_tile_walk(p.rows, p.cols);
   if (tw.ntiles == 0) return hipSuccess;
-  auto kernel = in_fmt == kE4M3
-                    ? (fmt == kE4M3 ? recast_kernel<kE4M3, kE4M3> : recast_kernel<kE4M3, kE5M2>)
-                    : (fmt == kE4M3 ? recast_kernel<kE5M2, kE4M3> : recast_kernel<kE5M2, kE5M2>);
+  const bool any = p.out.lay.flags != 0;
+  auto kernel = in_fmt == kE4M3 ? (fmt == kE4M3 ? pick<kE4M3, kE4M3>(any) : pick<kE4M3, kE5M2>(any))
+                                : (fmt == kE4M3 ? pick<kE5M2, kE4M3>(any) : pick<kE5M2, kE5M2>(any));
   launch_kernel(kernel, dim3(tw.per_xcd * kTileXcds), dim3(kThreads), 0, stream, p, tw);
   return hipGetLastError();
 }

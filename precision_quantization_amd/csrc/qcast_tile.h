@@ -18,18 +18,33 @@ namespace qcast {
 constexpr uint32_t kTile = 128;              // tokens and channels of a tile
 constexpr uint32_t kTileXcds = 8;
 
-// Tile walk: each XCD takes a contiguous range of tiles, token groups
-// fastest, so neighbouring tokens' lines of one channel row meet in one L2.
+// Tile walk: each XCD takes a contiguous range of tiles, in strips of `strip`
+// channel tiles: token group outer, channel tile inner.
 struct TileWalk {
-  uint32_t ntg, nct, ntiles, per_xcd;
+  uint32_t ntg, nct, ntiles, per_xcd, strip;
+  FastDiv strip_div;       // by strip * ntg
 };
-inline TileWalk make_tile_walk(int64_t rows, int64_t cols) {
+struct TilePos {
+  uint32_t ct, gt;
+};
+inline TileWalk make_tile_walk(int64_t rows, int64_t cols, uint32_t strip) {
   TileWalk w;
   w.ntg = (uint32_t)((rows + kTile - 1) / kTile);
   w.nct = (uint32_t)((cols + kTile - 1) / kTile);
   w.ntiles = w.ntg * w.nct;
   w.per_xcd = (w.ntiles + kTileXcds - 1) / kTileXcds;
+  w.strip = strip;
+  w.strip_div = make_fast_div(w.ntg * strip ? w.ntg * strip : 1);
   return w;
+}
+__device__ __forceinline__ TilePos tile_pos(uint32_t tau, const TileWalk& w) {
+  const uint32_t s = fast_div(tau, w.strip_div);
+  const uint32_t rem = tau - s * w.strip * w.ntg;
+  const uint32_t width = w.nct - s * w.strip < w.strip ? w.nct - s * w.strip : w.strip;
+  TilePos p;
+  p.gt = rem / width;
+  p.ct = s * w.strip + (rem - p.gt * width);
+  return p;
 }
 
 constexpr uint32_t kTileRowDw = 36;

@@ -21,6 +21,11 @@
 namespace qcast {
 namespace {
 
+#ifndef QCAST_RC_STRIP
+#define QCAST_RC_STRIP 2
+#endif
+constexpr uint32_t kStrip = QCAST_RC_STRIP;
+
 // The fp32 value of code j (0..15) of a token's 16 codes.
 template <int kIn>
 __device__ __forceinline__ void decode_word(uint32_t w, float sf, float v[4]) {
@@ -36,7 +41,8 @@ __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk
   __shared__ float inv_s[kTile];
   const uint32_t tau = (blockIdx.x % kTileXcds) * tw.per_xcd + blockIdx.x / kTileXcds;
   if (tau >= tw.ntiles) return;
-  const uint32_t ct = tau / tw.ntg, gt = tau - ct * tw.ntg;
+  const TilePos tp = tile_pos(tau, tw);
+  const uint32_t ct = tp.ct, gt = tp.gt;
   const uint32_t c0 = ct * kTile, t0 = gt * kTile;
   const uint32_t nc = p.cols - c0 < kTile ? p.cols - c0 : kTile;
   const uint32_t ch = threadIdx.x & 7;           // 16-channel chunk
@@ -57,26 +63,37 @@ __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk
       sf[i] = p.sf[(uint64_t)t * gpr + ((c0 + ch * 16) >> (p.shift + 3))];
     }
   }
-  // column maxima of the lane's 4 tokens, then over the 8 lanes of the wave
-  // that hold the same channels
+  // Column maxima of the lane's 4 tokens, then over the 8 lanes of the wave
+  // that hold the same 16 channels (lane bits 3, 4, 5), as a butterfly whose
+  // exchanges carry two channels each: a lane ends with two of the 16.
+  uint32_t m[16];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float t[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[4];
-      decode_word<kIn>(raw[i][w], sf[i], v);
+    for (int i = 0; i < 4; ++i) decode_word<kIn>(raw[i][w], sf[i], t[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], fabsf(v[j]));
-    }
+    for (int j = 0; j < 4; ++j)
+      m[4 * w + j] = __float_as_uint(fmaxf(fmaxf(fabsf(t[0][j]), fabsf(t[1][j])),
+                                           fmaxf(fabsf(t[2][j]), fabsf(t[3][j]))));
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t b = __float_as_uint(m[j]);
-      b = umax(b, dpp<kDppRor8>(b));
-      b = max_xor16(b);
-      b = max_xor32(b);
-      if ((threadIdx.x & 63) < 8) amax_s[threadIdx.x >> 6][ch * 16 + 4 * w + j] = __uint_as_float(b);
-    }
+  for (int j = 0; j < 8; ++j) {        // bit 4: upper 8 channels
+    const auto r = __builtin_amdgcn_permlane16_swap(m[j], m[j + 8], false, false);
+    m[j] = umax((uint32_t)r[0], (uint32_t)r[1]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {        // bit 5: upper 4 of those
+    const auto r = __builtin_amdgcn_permlane32_swap(m[j], m[j + 4], false, false);
+    m[j] = umax((uint32_t)r[0], (uint32_t)r[1]);
+  }
+  const bool odd = (threadIdx.x & 8) != 0;   // bit 3: upper 2 of those
+  const uint32_t c2 = ch * 16 + ((threadIdx.x >> 4) & 1) * 8 + ((threadIdx.x >> 5) & 1) * 4 +
+                      (odd ? 2 : 0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t keep = odd ? m[j + 2] : m[j], send = odd ? m[j] : m[j + 2];
+    amax_s[threadIdx.x >> 6][c2 + j] = __uint_as_float(umax(keep, dpp<kDppRor8>(send)));
   }
   __syncthreads();
   if (threadIdx.x < kTile) {
@@ -124,7 +141,7 @@ bool tile_fits(int64_t rows, int64_t cols, int64_t stride) {
 }
 
 hipError_t launch_recast(const RecastTile& p, int in_fmt, int fmt, hipStream_t stream) {
-  const TileWalk tw = make_tile_walk(p.rows, p.cols);
+  const TileWalk tw = make_tile_walk(p.rows, p.cols, kStrip);
   if (tw.ntiles == 0) return hipSuccess;
   const bool any = p.out.lay.flags != 0;
   auto kernel = in_fmt == kE4M3 ? (fmt == kE4M3 ? pick<kE4M3, kE4M3>(any) : pick<kE4M3, kE5M2>(any))

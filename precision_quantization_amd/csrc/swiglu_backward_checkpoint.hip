@@ -26,6 +26,11 @@
 namespace qcast {
 namespace {
 
+#ifndef QCAST_SBC_STRIP
+#define QCAST_SBC_STRIP 4
+#endif
+constexpr uint32_t kStrip = QCAST_SBC_STRIP;
+
 constexpr int kBlock = 512;
 constexpr int kWaves = kBlock / 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -133,7 +138,8 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   __shared__ float inv_s[3 * kTile];
   const uint32_t tau = (blockIdx.x % kTileXcds) * tw.per_xcd + blockIdx.x / kTileXcds;
   if (tau >= tw.ntiles) return;
-  const uint32_t ct = tau / tw.ntg, gt = tau - ct * tw.ntg;
+  const TilePos tp = tile_pos(tau, tw);
+  const uint32_t ct = tp.ct, gt = tp.gt;
   const uint32_t c0 = ct * kTile, t0 = gt * kTile;
   const uint32_t ch = threadIdx.x & 15;          // 8-channel chunk
   const uint32_t quad = threadIdx.x >> 4;        // 4 tokens
@@ -278,6 +284,7 @@ __global__ __launch_bounds__(kThreads) void row_weight_join_kernel(const float* 
   const uint32_t r = blockIdx.x * kThreads + threadIdx.x;
   if (r >= rows) return;
   float s = ws[r];
+#pragma unroll 16
   for (uint32_t i = 1; i < nct; ++i) s += ws[(uint64_t)i * rows + r];
   dw[r] = s;
 }
@@ -299,7 +306,7 @@ auto pick(const SwigluTile& p) {
 
 hipError_t launch_swiglu_backward_checkpoint(const SwigluTile& p, int ckpt_fmt, int fmt,
                                              hipStream_t stream) {
-  const TileWalk tw = make_tile_walk(p.rows, p.cols);
+  const TileWalk tw = make_tile_walk(p.rows, p.cols, kStrip);
   if (tw.ntiles == 0) return hipSuccess;
   auto kernel = ckpt_fmt == kE4M3
                     ? (fmt == kE4M3 ? pick<kE4M3, kE4M3>(p) : pick<kE4M3, kE5M2>(p))

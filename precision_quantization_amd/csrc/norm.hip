@@ -16,10 +16,14 @@
 // element with 8-bit codes, 9 with both 8-bit checkpoints), so it is bound by
 // HBM bandwidth, or by the launch for a few rows.
 //
-// gfx950 design. One workgroup per row: a lane holds kC chunks of 8 columns
-// in registers from the one load to the last store, so the row crosses HBM
-// once although it is reduced twice. Each sum is a wave butterfly and one
-// LDS exchange (the two use separate words, one barrier each).
+// gfx950 design. A workgroup holds a row in registers from the load to the
+// last store (a lane kC chunks of 8 columns), so the row crosses HBM once
+// although it is reduced twice; each sum is a wave butterfly and one LDS trip.
+// It walks the rows with a stride of the grid, which leaves the columns'
+// factors in registers and lets the next row be loaded while this one is
+// worked on. The up to three casts of a chunk (x and the two checkpoints)
+// need three scales: lane j of a quad forms the j-th and the quad exchanges
+// them, so a lane runs the scale's 30 instructions once.
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -27,110 +31,179 @@
 namespace qcast {
 namespace {
 
+#ifndef QCAST_NF_WAVES
+#define QCAST_NF_WAVES 28
+#endif
 constexpr int kMaxWaves = 16;
 
-// Sum over the workgroup, the same bits in every thread.
-__device__ __forceinline__ float block_sum(float v, float* part) {
-  v = wave_sum(v);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = part[0];
-  for (int i = 1; i < waves; ++i) s += part[i];
-  return s;
+// The value lane j of the quad holds.
+template <int kJ>
+__device__ __forceinline__ float from_quad(float v) {
+  return __uint_as_float(dpp<kJ * 0x55>(__float_as_uint(v)));
 }
 
-template <int kC>
-__global__ __launch_bounds__(1024) void norm_kernel(NormForward p) {
-  __shared__ float part[2][kMaxWaves];
-  const uint32_t row = blockIdx.x;
+struct RowChunk {
+  u32x4 y, h, gate;
+};
+template <int kGate, bool kY>
+__device__ __forceinline__ RowChunk load_row_chunk(const NormForward& p, uint32_t row,
+                                                   uint32_t jc, bool valid) {
+  const int64_t at = (int64_t)row * p.chunks + jc;
+  RowChunk c;
+  c.y = c.h = c.gate = u32x4{0u, 0u, 0u, 0u};
+  if (!valid) return c;
+  if (kY) c.y = load_stream(reinterpret_cast<const u32x4*>(p.y) + at);
+  c.h = load_stream(reinterpret_cast<const u32x4*>(p.h) + at);
+  if (kGate == kGateFull) c.gate = load_stream(reinterpret_cast<const u32x4*>(p.gate) + at);
+  return c;
+}
+
+// kGate: kGateFull, kGateToken, or kGateNone for both other kinds (a channel
+// gate is one of the column factors). kY: there is a block output. kCkpt: the
+// checkpoints' format, 0 for none.
+#ifndef QCAST_NF_MIN
+#define QCAST_NF_MIN 4
+#endif
+template <int kC, int kGate, bool kY, int kCkpt>
+__global__ __launch_bounds__(1024, kC == 1 ? QCAST_NF_MIN : 4) void norm_kernel(NormForward p, uint32_t rows) {
+  constexpr bool kAhead = kC == 1;
+  __shared__ float part[4][kMaxWaves];
+  int buf = 0;             // alternates, so that a row's words outlive its last reader
   const uint32_t chunks = p.chunks;
-  const u32x4* hr = reinterpret_cast<const u32x4*>(p.h) + (int64_t)row * chunks;
-  const u32x4* yr = reinterpret_cast<const u32x4*>(p.y) + (int64_t)row * chunks;
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  u32x4 hraw[kC], yraw[kC], wq[kC], wp[kC], gt[kC];
-  float hv[kC][8];
+  float c[kC][8], q[kC][8];
 #pragma unroll
   for (int k = 0; k < kC; ++k) {
     const uint32_t jc = threadIdx.x + k * blockDim.x;
     const bool valid = jc < chunks;
-    yraw[k] = (valid && p.y) ? load_stream(yr + jc) : zero;
-    hraw[k] = valid ? load_stream(hr + jc) : zero;
-    wp[k] = (valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero;
-    gt[k] = zero;
-    if (valid && p.gate_kind == kGateChannel)
-      gt[k] = reinterpret_cast<const u32x4*>(p.gate)[jc];
-    else if (valid && p.gate_kind == kGateFull)
-      gt[k] = load_stream(reinterpret_cast<const u32x4*>(p.gate) + (int64_t)row * chunks + jc);
-    wq[k] = valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero;
-  }
-  const float row_gate =
-      p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
-
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    unpack8(valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero, q[k]);
+    unpack8((valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero, c[k]);
 #pragma unroll
-  for (int k = 0; k < kC; ++k) unpack8(hraw[k], hv[k]);
-  if (p.y) {
-    float r1 = 1.0f;
-    if (p.w_post) {
-      float ss = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      q[k][i] = q[k][i] + p.offset;
+      c[k][i] = p.w_post ? c[k][i] + p.offset : 1.0f;
+    }
+    if (p.gate_kind == kGateChannel) {
+      float g[8];
+      unpack8(valid ? reinterpret_cast<const u32x4*>(p.gate)[jc] : zero, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[k][i] = c[k][i] * g[i];
+    }
+  }
+  // lane j of a quad: the scale of x (0), of y's checkpoint (1), of h's (2)
+  const int j = threadIdx.x & 3;
+  const ScaleRule rule = (kCkpt && j) ? scale_rule(kCkpt, p.h_ckpt.floor)
+                                      : scale_rule(p.cast.fmt, p.cast.floor);
+  RowChunk next;
+  if (kAhead)
+    next = load_row_chunk<kGate, kY>(p, blockIdx.x, threadIdx.x, threadIdx.x < chunks);
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 2) {
+    RowChunk ch[kC];
+    const float row_gate = kGate == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
+    if constexpr (kAhead) {
+      ch[0] = next;
+      if (row + gridDim.x < rows)
+        next = load_row_chunk<kGate, kY>(p, row + gridDim.x, threadIdx.x, threadIdx.x < chunks);
+    } else {
 #pragma unroll
       for (int k = 0; k < kC; ++k) {
-        float v[8];
-        unpack8(yraw[k], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+        const uint32_t jc = threadIdx.x + k * blockDim.x;
+        ch[k] = load_row_chunk<kGate, kY>(p, row, jc, jc < chunks);
       }
-      ss = block_sum(ss, part[0]);
-      r1 = 1.0f / sqrtf(ss / p.n + p.eps);
-      if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r1;
     }
+    float hv[kC][8], y[kC][8];
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+      unpack8(ch[k].h, hv[k]);
+      if (kY) unpack8(ch[k].y, y[k]);
+    }
+    if constexpr (kY) {
+      float r1 = 1.0f;
+      if (p.w_post) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kC; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(y[k][i], y[k][i], ss);
+        ss = block_sum(ss, part[buf]);
+        r1 = inv_sqrt(__builtin_fmaf(ss, p.inv_n, p.eps));
+        if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r1;
+      }
+      if (kGate == kGateToken) r1 = r1 * row_gate;
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        float g[8];
+        if (kGate == kGateFull) unpack8(ch[k].gate, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float t = y[k][i] * r1 * c[k][i];
+          if (kGate == kGateFull) t = t * g[i];
+          hv[k][i] = __builtin_fmaf(p.alpha, hv[k][i], t);
+        }
+      }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kC; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(hv[k][i], hv[k][i], ss);
+    ss = block_sum(ss, part[buf + 1]);
+    const float r2 = inv_sqrt(__builtin_fmaf(ss, p.inv_n, p.eps));
+    if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r2;
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
-      float y[8], w[8], g[8];
-      unpack8(yraw[k], y);
-      unpack8(wp[k], w);
-      unpack8(gt[k], g);
-      if (p.y_ckpt.q && jc < chunks) checkpoint_chunk(p.y_ckpt, row, jc, chunks, y);
+      const int64_t at = (int64_t)row * chunks + jc;
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float t = y[i];
-        if (p.w_post) t = t * r1 * (w[i] + p.offset);
-        if (p.gate_kind == kGateChannel || p.gate_kind == kGateFull) t = t * g[i];
-        t = t * row_gate;
-        hv[k][i] = p.alpha * hv[k][i] + t;
+      for (int i = 0; i < 8; ++i) x[i] = hv[k][i] * r2 * q[k][i];
+      if (jc >= chunks) continue;      // the lanes of a scale group leave together
+      if (kY) store_stream(reinterpret_cast<u32x4*>(p.h_out) + at, pack8_bf16(hv[k]));
+      if (p.x_out) store_stream(reinterpret_cast<u32x4*>(p.x_out) + at, pack8_bf16(x));
+      float amax = run_max(absmax8(x), p.cast.shift);
+      if (kCkpt) {
+        const float ha = lane_group_max<16>(absmax8(hv[k]));
+        amax = j == 2 ? ha : amax;
+        if (kY) {
+          const float ya = lane_group_max<16>(absmax8(y[k]));
+          amax = j == 1 ? ya : amax;
+        }
       }
-      if (jc < chunks)
-        store_stream(reinterpret_cast<u32x4*>(p.h_out) + (int64_t)row * chunks + jc,
-                     pack8_bf16(hv[k]));
+      Scale s = scale_by(rule, amax);
+      if ((p.cast.lay.flags & kSfRound) && !(kCkpt && j)) s = round_scale_pow2(s);
+      if (p.cast.q) {
+        encode_chunk_any(p.cast, at, x, kCkpt ? from_quad<0>(s.inv) : s.inv);
+        store_run_scale(p.cast.sf, row, jc >> p.cast.shift, s, p.cast.lay, p.cast.shift);
+      }
+      if constexpr (kCkpt != 0) {
+        const int64_t sat = (int64_t)row * (chunks / 16) + jc / 16;
+        const int l = threadIdx.x & 15;
+        if (p.h_ckpt.q) {
+          encode_chunk<kCkpt>(p.h_ckpt, at, hv[k], from_quad<2>(s.inv));
+          if (l == 2) static_cast<float*>(p.h_ckpt.sf)[sat] = s.sf;
+        }
+        if (kY && p.y_ckpt.q) {
+          encode_chunk<kCkpt>(p.y_ckpt, at, y[k], from_quad<1>(s.inv));
+          if (l == 1) static_cast<float*>(p.y_ckpt.sf)[sat] = s.sf;
+        }
+      }
     }
   }
+}
 
-  float ss = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kC; ++k) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(hv[k][i], hv[k][i], ss);
-  }
-  ss = block_sum(ss, part[1]);
-  const float r2 = 1.0f / sqrtf(ss / p.n + p.eps);
-  if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r2;
-#pragma unroll
-  for (int k = 0; k < kC; ++k) {
-    const uint32_t jc = threadIdx.x + k * blockDim.x;
-    if (jc < chunks) {
-      float v[8], w[8];
-      unpack8(wq[k], w);
-      if (p.h_ckpt.q) checkpoint_chunk(p.h_ckpt, row, jc, chunks, hv[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = hv[k][i] * r2 * (w[i] + p.offset);
-      if (p.x_out)
-        store_stream(reinterpret_cast<u32x4*>(p.x_out) + (int64_t)row * chunks + jc,
-                     pack8_bf16(v));
-      if (p.cast.q) cast_chunk(p.cast, row, jc, chunks, v);
-    }
-  }
+template <int kC, int kGate, bool kY>
+auto pick_ckpt(const NormForward& p) {
+  const int f = (p.h_ckpt.q || p.y_ckpt.q) ? p.h_ckpt.fmt : 0;
+  return f == 0       ? norm_kernel<kC, kGate, kY, 0>
+         : f == kE4M3 ? norm_kernel<kC, kGate, kY, kE4M3>
+                      : norm_kernel<kC, kGate, kY, kE5M2>;
+}
+template <int kC>
+auto pick(const NormForward& p) {
+  return !p.y                        ? pick_ckpt<kC, kGateNone, false>(p)
+         : p.gate_kind == kGateFull  ? pick_ckpt<kC, kGateFull, true>(p)
+         : p.gate_kind == kGateToken ? pick_ckpt<kC, kGateToken, true>(p)
+                                     : pick_ckpt<kC, kGateNone, true>(p);
 }
 
 }  // namespace
@@ -138,10 +211,14 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p) {
 hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream) {
   if (rows == 0 || p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
-  const int kc = p.chunks > 2048 ? 4 : p.chunks > 256 ? 2 : 1;
+  const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
   const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
-  auto kernel = kc == 1 ? norm_kernel<1> : kc == 2 ? norm_kernel<2> : norm_kernel<4>;
-  launch_kernel(kernel, dim3((unsigned)rows), dim3(threads), 0, stream, p);
+  // as many workgroups as run at once on the 256 compute units
+  const int64_t resident = (int64_t)256 * (QCAST_NF_WAVES / (threads / 64) > 0
+                                               ? QCAST_NF_WAVES / (threads / 64) : 1);
+  const unsigned grid = (unsigned)(rows < resident ? rows : resident);
+  auto kernel = kc == 1 ? pick<1>(p) : kc == 2 ? pick<2>(p) : pick<4>(p);
+  launch_kernel(kernel, dim3(grid), dim3(threads), 0, stream, p, (uint32_t)rows);
   return hipGetLastError();
 }
 

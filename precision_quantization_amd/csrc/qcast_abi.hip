@@ -619,7 +619,7 @@ int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t col
   p.alpha = residual_scale;
   p.offset = weight_offset;
   p.eps = eps;
-  p.n = (float)cols;
+  p.inv_n = 1.0f / (float)cols;
   p.chunks = (uint32_t)(cols / 8);
   return finish(qcast::launch_norm(p, rows, static_cast<hipStream_t>(stream)));
 }

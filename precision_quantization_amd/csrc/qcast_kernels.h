@@ -202,7 +202,7 @@ struct NormForward {
   RowCast cast, y_ckpt, h_ckpt;
   int gate_kind;
   float alpha, offset, eps;
-  float n;                   // cols
+  float inv_n;               // 1 / cols
   uint32_t chunks;           // cols / 8
 };
 hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream);

@@ -126,44 +126,84 @@ __device__ __forceinline__ void store_run_scale(void* sf, uint32_t r, uint32_t k
 }
 
 template <int kFmt>
-__device__ __forceinline__ void cast_chunk_fmt(const RowCast& rc, uint32_t row, uint32_t jc,
-                                               uint32_t chunks, float amax, const float v[8]) {
-  Scale s = group_scale<kFmt>(amax, rc.floor);
-  if (rc.lay.flags & kSfRound) s = round_scale_pow2(s);
+__device__ __forceinline__ void encode_chunk(const RowCast& rc, int64_t chunk, const float v[8],
+                                             float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = v[i] * s.inv;
-  store_chunk8<kFmt>(rc.q, (int64_t)row * chunks + jc, y);
-  store_run_scale(rc.sf, row, jc >> rc.shift, s, rc.lay, rc.shift);
+  for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
+  store_chunk8<kFmt>(rc.q, chunk, y);
+}
+// Codes of a chunk in the cast's format, with the inverse scale known.
+__device__ __forceinline__ void encode_chunk_any(const RowCast& rc, int64_t chunk,
+                                                 const float v[8], float inv) {
+  switch (rc.fmt) {
+    case kE4M3: encode_chunk<kE4M3>(rc, chunk, v, inv); break;
+    case kE5M2: encode_chunk<kE5M2>(rc, chunk, v, inv); break;
+    case kE2M1: encode_chunk<kE2M1>(rc, chunk, v, inv); break;
+    default: encode_chunk<kE5M6>(rc, chunk, v, inv); break;
+  }
+}
+
+// group_scale with the format at run time, and possibly another one in every
+// lane: its constants are values (the same sequence, so the same bits).
+struct ScaleRule {
+  float floor, max, recip, lo, hi;
+};
+__device__ __forceinline__ ScaleRule scale_rule(int fmt, float floor) {
+  ScaleRule r;
+  r.floor = floor;
+  r.max = fmt == kE4M3 ? kE4M3Max : fmt == kE5M2 ? kE5M2Max : fmt == kE2M1 ? kE2M1Max : kE5M6Max;
+  r.recip = fmt == kE4M3   ? 1.0f / kE4M3Max
+            : fmt == kE5M2 ? 1.0f / kE5M2Max
+            : fmt == kE2M1 ? 1.0f / kE2M1Max
+                           : 1.0f / kE5M6Max;
+  r.lo = r.max * 0x1.0p-126f;
+  r.hi = fmt == kE2M1 ? kE2M1Max * 0x1.0p124f : __builtin_huge_valf();
+  return r;
+}
+__device__ __forceinline__ Scale scale_by(const ScaleRule& r, float amax) {
+  const float a = amax < r.floor ? r.floor : amax;
+  Scale s;
+  if (a >= r.lo && a < r.hi) {
+    const float q0 = a * r.recip;
+    s.sf = __builtin_fmaf(__builtin_fmaf(-q0, r.max, a), r.recip, q0);
+    const float y0 = __builtin_amdgcn_rcpf(s.sf);
+    s.inv = __builtin_fmaf(__builtin_fmaf(-s.sf, y0, 1.0f), y0, y0);
+  } else {
+    s.sf = a / r.max;
+    s.inv = 1.0f / s.sf;
+  }
+  return s;
 }
 
 // Cast chunk jc (columns 8 jc .. 8 jc + 7) of row `row` (of `chunks` chunks).
 // The lanes of a scale group call this together, lane = jc mod 64.
 __device__ __forceinline__ void cast_chunk(const RowCast& rc, uint32_t row, uint32_t jc,
                                            uint32_t chunks, const float v[8]) {
-  const float amax = run_max(absmax8(v), rc.shift);
-  switch (rc.fmt) {
-    case kE4M3: cast_chunk_fmt<kE4M3>(rc, row, jc, chunks, amax, v); break;
-    case kE5M2: cast_chunk_fmt<kE5M2>(rc, row, jc, chunks, amax, v); break;
-    case kE2M1: cast_chunk_fmt<kE2M1>(rc, row, jc, chunks, amax, v); break;
-    default: cast_chunk_fmt<kE5M6>(rc, row, jc, chunks, amax, v); break;
-  }
+  Scale s = scale_by(scale_rule(rc.fmt, rc.floor), run_max(absmax8(v), rc.shift));
+  if (rc.lay.flags & kSfRound) s = round_scale_pow2(s);
+  encode_chunk_any(rc, (int64_t)row * chunks + jc, v, s.inv);
+  store_run_scale(rc.sf, row, jc >> rc.shift, s, rc.lay, rc.shift);
 }
 
-// The same into one of the two 8-bit formats with plain row-major scales (a
-// checkpoint).
-__device__ __forceinline__ void checkpoint_chunk(const RowCast& rc, uint32_t row, uint32_t jc,
-                                                 uint32_t chunks, const float v[8]) {
-  const float amax = run_max(absmax8(v), rc.shift);
-  const bool e4 = rc.fmt == kE4M3;
-  const Scale s = e4 ? group_scale<kE4M3>(amax, rc.floor) : group_scale<kE5M2>(amax, rc.floor);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = v[i] * s.inv;
-  if (e4) store_chunk8<kE4M3>(rc.q, (int64_t)row * chunks + jc, y);
-  else store_chunk8<kE5M2>(rc.q, (int64_t)row * chunks + jc, y);
-  if ((threadIdx.x & ((1 << rc.shift) - 1)) == 0)
-    static_cast<float*>(rc.sf)[(int64_t)row * rc.lay.gpr + (jc >> rc.shift)] = s.sf;
+// 1 / sqrt(v) for normal v > 0: the hardware's root (1 ulp) and one Newton
+// step on its residual. 0 gives infinity and infinity 0, as the quotient does.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = __builtin_amdgcn_rsqf(v);
+  const float e = __builtin_fmaf(-v * r, r, 1.0f);
+  const float c = __builtin_fmaf(0.5f * r, e, r);
+  return (v > 0.0f && v < __builtin_huge_valf()) ? c : r;
+}
+
+// Sum over the workgroup (at most 16 waves), the same bits in every thread.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = wave_sum(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  const int i = threadIdx.x & 15;
+  return row16_sum(i < waves ? part[i] : 0.0f);
 }
 
 }  // namespace qcast

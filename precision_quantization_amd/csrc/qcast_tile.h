@@ -70,7 +70,8 @@ __device__ __forceinline__ float channel_scale(void* sf, const SfLayout& lay, ui
 
 // Store the LDS tile's channel rows [c0, c0 + nc) of token group gt, 16
 // tokens per lane. rows_T: codes per channel row. kN threads call this.
-template <int kN>
+// kStream: past the caches; else with plain stores.
+template <int kN, bool kStream>
 __device__ __forceinline__ void store_tile_rows(const uint32_t* tile, uint8_t* qT, uint32_t c0,
                                                 uint32_t nc, uint32_t gt, uint32_t rows_T) {
   uint8_t* out = qT + (uint64_t)c0 * rows_T + gt * kTile;
@@ -80,7 +81,9 @@ __device__ __forceinline__ void store_tile_rows(const uint32_t* tile, uint8_t* q
     const uint32_t c = idx / 8, v = idx % 8;
     if (c < nc) {
       const u32x4 val = *reinterpret_cast<const u32x4*>(tile + swizzled(c, 4 * v));
-      store_stream(reinterpret_cast<u32x4*>(out + c * rows_T + 16 * v), val);
+      u32x4* to = reinterpret_cast<u32x4*>(out + c * rows_T + 16 * v);
+      if (kStream) store_stream(to, val);
+      else *to = val;
     }
   }
 }

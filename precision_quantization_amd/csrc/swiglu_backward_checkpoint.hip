@@ -271,17 +271,17 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   if (p.v.qT) put_codes<kFmt>(v, inv_s + 2 * kTile + ch * 8, ch * 8, quad, tile[2]);
   __syncthreads();
   if (p.dh.qT) {
-    store_tile_rows<kBlock>(tile[0], p.dh.qT, c0, kTile, gt, rows_T);
-    store_tile_rows<kBlock>(tile[1], p.dh.qT, c0 + cols, kTile, gt, rows_T);
+    store_tile_rows<kBlock, true>(tile[0], p.dh.qT, c0, kTile, gt, rows_T);
+    store_tile_rows<kBlock, true>(tile[1], p.dh.qT, c0 + cols, kTile, gt, rows_T);
   }
-  if (p.v.qT) store_tile_rows<kBlock>(tile[2], p.v.qT, c0, kTile, gt, rows_T);
+  if (p.v.qT) store_tile_rows<kBlock, true>(tile[2], p.v.qT, c0, kTile, gt, rows_T);
 }
 
 // dw[r] = sum over the channel tiles of their partial sums, in tile order.
-__global__ __launch_bounds__(kThreads) void row_weight_join_kernel(const float* __restrict__ ws,
+__global__ __launch_bounds__(64) void row_weight_join_kernel(const float* __restrict__ ws,
                                                                    uint32_t rows, uint32_t nct,
                                                                    float* __restrict__ dw) {
-  const uint32_t r = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = blockIdx.x * 64 + threadIdx.x;
   if (r >= rows) return;
   float s = ws[r];
 #pragma unroll 16
@@ -314,8 +314,8 @@ hipError_t launch_swiglu_backward_checkpoint(const SwigluTile& p, int ckpt_fmt, 
   launch_kernel(kernel, dim3(tw.per_xcd * kTileXcds), dim3(kBlock), 0, stream, p, tw);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.dw || tw.nct == 1) return err;
-  launch_kernel(row_weight_join_kernel, dim3((p.rows + kThreads - 1) / kThreads), dim3(kThreads),
-                0, stream, (const float*)p.ws, p.rows, tw.nct, p.dw);
+  launch_kernel(row_weight_join_kernel, dim3((p.rows + 63) / 64), dim3(64), 0, stream,
+                (const float*)p.ws, p.rows, tw.nct, p.dw);
   return hipGetLastError();
 }
 

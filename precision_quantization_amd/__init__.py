@@ -545,13 +545,17 @@ def _placed(device, stream):
     """The handle of the stream a call runs on and the context in which it
     allocates: outputs and workspaces come from that stream's pool, so memory
     still in use on the current stream is never handed to another one."""
-    current = torch.cuda.current_stream(device)
-    handle = current.cuda_stream if stream is None else _stream(device, stream)
-    if handle != current.cuda_stream:
+    here = torch.cuda.current_device()
+    if device.index == here:
+        current = torch._C._cuda_getCurrentRawStream(here)     # 2 us less than a Stream object
+    else:
+        current = torch.cuda.current_stream(device).cuda_stream
+    handle = current if stream is None else _stream(device, stream)
+    if handle != current:
         s = torch.cuda.default_stream(device) if handle == 0 else \
             torch.cuda.ExternalStream(handle, device=device)
         return handle, torch.cuda.stream(s)
-    if device.index != torch.cuda.current_device():
+    if device.index != here:
         return handle, torch.cuda.device(device)
     return handle, _HERE
 

@@ -32,7 +32,13 @@ namespace qcast {
 namespace {
 
 #ifndef QCAST_NF_WAVES
-#define QCAST_NF_WAVES 28
+#define QCAST_NF_WAVES 16
+#endif
+#ifndef QCAST_NF_AHEAD
+#define QCAST_NF_AHEAD 1
+#endif
+#ifndef QCAST_NF_T2
+#define QCAST_NF_T2 1024
 #endif
 constexpr int kMaxWaves = 16;
 
@@ -66,7 +72,7 @@ __device__ __forceinline__ RowChunk load_row_chunk(const NormForward& p, uint32_
 #endif
 template <int kC, int kGate, bool kY, int kCkpt>
 __global__ __launch_bounds__(1024, kC == 1 ? QCAST_NF_MIN : 4) void norm_kernel(NormForward p, uint32_t rows) {
-  constexpr bool kAhead = kC == 1;
+  constexpr bool kAhead = kC <= QCAST_NF_AHEAD;
   __shared__ float part[4][kMaxWaves];
   int buf = 0;             // alternates, so that a row's words outlive its last reader
   const uint32_t chunks = p.chunks;
@@ -94,16 +100,25 @@ __global__ __launch_bounds__(1024, kC == 1 ? QCAST_NF_MIN : 4) void norm_kernel(
   const int j = threadIdx.x & 3;
   const ScaleRule rule = (kCkpt && j) ? scale_rule(kCkpt, p.h_ckpt.floor)
                                       : scale_rule(p.cast.fmt, p.cast.floor);
-  RowChunk next;
-  if (kAhead)
-    next = load_row_chunk<kGate, kY>(p, blockIdx.x, threadIdx.x, threadIdx.x < chunks);
+  RowChunk next[kC];
+  if (kAhead) {
+#pragma unroll
+    for (int k = 0; k < kC; ++k) {
+      const uint32_t jc = threadIdx.x + k * blockDim.x;
+      next[k] = load_row_chunk<kGate, kY>(p, blockIdx.x, jc, jc < chunks);
+    }
+  }
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 2) {
     RowChunk ch[kC];
     const float row_gate = kGate == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
     if constexpr (kAhead) {
-      ch[0] = next;
-      if (row + gridDim.x < rows)
-        next = load_row_chunk<kGate, kY>(p, row + gridDim.x, threadIdx.x, threadIdx.x < chunks);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        const uint32_t jc = threadIdx.x + k * blockDim.x;
+        ch[k] = next[k];
+        if (row + gridDim.x < rows)
+          next[k] = load_row_chunk<kGate, kY>(p, row + gridDim.x, jc, jc < chunks);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < kC; ++k) {
@@ -211,7 +226,7 @@ auto pick(const NormForward& p) {
 hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream) {
   if (rows == 0 || p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
-  const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
+  const int kc = p.chunks > 2048 ? 4 : p.chunks > QCAST_NF_T2 ? 2 : 1;
   const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
   // as many workgroups as run at once on the 256 compute units
   const int64_t resident = (int64_t)256 * (QCAST_NF_WAVES / (threads / 64) > 0

@@ -1,0 +1,264 @@
+"""The checkpoint and norm operators together, as a training step uses them:
+norm -> product -> SwiGLU with checkpoint -> product, and back through the
+SwiGLU backward, the recast input and the norm backward to both residual
+inputs and the weights. Also on another stream, from two threads, captured in a
+graph, and between poisoned guard bands."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import block_ref as br
+import precision_quantization_amd as pq
+
+pytestmark = pytest.mark.gpu
+GUARD, POISON = 4096, 0x5A
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def dec(q, sf, group=128):
+    """Codes and row-major scales -> fp32 values."""
+    return q.float() * sf.repeat_interleave(group, 1)
+
+
+def inputs(dev, rows=300, hidden=512, inter=256, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    t = dict(h=br.bf16(g, rows, hidden, std=2.0), y=br.bf16(g, rows, hidden), w_pre=br.bf16(g, hidden, std=0.2, mean=1.0),
+             w_post=br.bf16(g, hidden, std=0.2, mean=1.0), gate=br.bf16(g, hidden, std=0.5, mean=0.5),
+             w1=br.bf16(g, hidden, 2 * inter, std=hidden ** -0.5), w2=br.bf16(g, inter, hidden, std=inter ** -0.5),
+             rw=torch.rand(rows, generator=g), dy=br.bf16(g, rows, hidden), dh=br.bf16(g, rows, hidden))
+    return {k: v.to(dev) for k, v in t.items()}
+
+
+def step(t):
+    """One forward and backward step; every output that the library wrote."""
+    f = pq.qcast_norm_per_token(t["h"], t["w_pre"], t["y"], t["w_post"], t["gate"], residual_scale=0.9, ckpt_fmt="e4m3")
+    hh = torch.mm(dec(f.out, f.out_sf), t["w1"].float()).to(torch.bfloat16)
+    v, v_sf, ckpt, ckpt_sf = pq.qcast_swiglu_checkpoint(hh, t["rw"])
+    y1 = torch.mm(dec(v, v_sf), t["w2"].float())
+    dv = torch.mm(t["dy"].float(), t["w2"].float().t().contiguous()).to(torch.bfloat16)
+    b = pq.qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, t["rw"])
+    dx = torch.mm(dec(b.dh, b.dh_sf), t["w1"].float().t().contiguous()).to(torch.bfloat16)
+    xt, xt_sf = pq.qcast_recast_per_channel_T(f.out, f.out_sf)
+    dw1 = torch.mm(dec(xt, xt_sf), dec(b.dh_t, b.dh_t_sf).t().contiguous())
+    n = pq.qcast_norm_backward_per_token(dx, f.h_ckpt, f.rstd_pre, t["w_pre"], dh=t["dh"], saved_h_sf=f.h_ckpt_sf, saved_y=f.y_ckpt,
+                                         saved_y_sf=f.y_ckpt_sf, rstd_post=f.rstd_post, w_post=t["w_post"], gate=t["gate"],
+                                         residual_scale=0.9)
+    return dict(f._asdict(), v=v, v_sf=v_sf, ckpt=ckpt, ckpt_sf=ckpt_sf, y1=y1, dv=dv, dx=dx, xt=xt, xt_sf=xt_sf, dw1=dw1,
+                hh=hh, **{"b_" + k: x for k, x in b._asdict().items()}, **{"n_" + k: x for k, x in n._asdict().items()})
+
+
+def bits(o):
+    return {k: x.reshape(-1).view(torch.uint8).clone() for k, x in o.items() if x is not None}
+
+
+def test_step_against_the_formulas(dev):
+    t = inputs(dev)
+    o = step(t)
+    torch.cuda.synchronize()
+    c = {k: v.cpu().double() for k, v in t.items()}
+    f = br.norm_forward(c["h"], c["w_pre"], c["y"], c["w_post"], c["gate"], 0.9)
+    rows, hidden = f["x"].shape
+    # dW1 = x^T d: x is cast twice (per token, then along the tokens), d once.
+    # One cast: at most 2^-4 of the value or half the smallest step, plus the
+    # fp32 errors, far below 1% of either.
+    h64 = dec(o["ckpt"], o["ckpt_sf"]).cpu().double()
+    d64, _, dw64 = br.swiglu_grad(h64, o["dv"].cpu().double(), c["rw"])
+    e = 2.0 ** -4 * 1.01
+    top = lambda x, dim: x.abs().amax(dim, keepdim=True) / 448 * 2.0 ** -10 * 1.01
+    dx_abs = f["x"].abs() * ((1 + e) ** 2 - 1) + (1 + e) * top(f["x"], 1) + top(f["x"], 0) * (1 + e)
+    dd_abs = d64.abs() * e + top(d64, 0)
+    x, d = f["x"].abs(), d64.abs()
+    bound = (x + dx_abs).t() @ (d + dd_abs) - x.t() @ d
+    err = (o["dw1"].cpu().double() - f["x"].t() @ d64).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+    # and the errors average out: their size against the gradient's is that of
+    # independent roundings (at most 2^-4 / sqrt(3) each, three of them), not of
+    # a wrong sign or a missing term
+    assert err.norm() <= 0.1 * (f["x"].t() @ d64).norm()
+    # the routing weight's gradient is that of the loss sum(dv * v) in w
+    assert ((o["b_dw"].cpu().double() - dw64).abs() <= br.swiglu_grad_slack(h64, o["dv"].cpu().double(), c["rw"])[2]).all()
+    # the gradient of both residual inputs, from what was stored
+    hs = dec(o["h_ckpt"], o["h_ckpt_sf"]).cpu().double()
+    ys = dec(o["y_ckpt"], o["y_ckpt_sf"]).cpu().double()
+    args = (o["dx"].cpu().double(), c["dh"], hs, o["rstd_pre"].cpu().double(), c["w_pre"], ys, o["rstd_post"].cpu().double(),
+            c["w_post"], c["gate"], 0.9, 0.0, "channel")
+    want, slack = br.norm_backward(*args), br.norm_backward_slack(*args)
+    assert ((o["n_dh"].cpu().double() - want["dh"]).abs() <= want["dh"].abs() * 2.0 ** -8 + slack["dh"] * 1.01).all()
+    br.check_cast(br.raw(o["n_out"]), br.raw(o["n_out_sf"]), want["dy"].numpy(), "e4m3", 128, slack["dy"].numpy(), what="dy")
+    for k in ("dw_pre", "dw_post", "dgate"):
+        assert ((o["n_" + k].cpu().double() - want[k]).abs() <= slack[k] * 1.01).all(), k
+    # from the checkpoints the gradients differ from those of the unrounded
+    # activations by what one 8-bit rounding of xh and a does
+    exact = br.norm_backward(args[0], c["dh"], f["h"], f["r2"], c["w_pre"], c["y"], f["r1"], c["w_post"], c["gate"], 0.9, 0.0,
+                             "channel")
+    for k in ("dh", "dy", "dw_pre", "dw_post", "dgate"):
+        assert (want[k] - exact[k]).norm() <= 2.0 ** -4 * 1.5 * exact[k].norm(), k
+
+
+def test_step_on_another_stream(dev):
+    t = inputs(dev)
+    ref = bits(step(t))
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        got = bits(step(t))
+    side.synchronize()
+    assert all(torch.equal(got[k], ref[k]) for k in ref)
+
+
+def test_stream_argument(dev):
+    # the stream is named in the call while another one is current: outputs
+    # and workspaces belong to the named one
+    t = inputs(dev)
+    side = torch.cuda.Stream(dev)
+    ref = pq.qcast_norm_per_token(t["h"], t["w_pre"], t["y"], t["w_post"], t["gate"], ckpt_fmt="e4m3")
+    refb = pq.qcast_norm_backward_per_token(t["dy"], ref.h_ckpt, ref.rstd_pre, t["w_pre"], saved_h_sf=ref.h_ckpt_sf,
+                                            saved_y=ref.y_ckpt, saved_y_sf=ref.y_ckpt_sf, rstd_post=ref.rstd_post,
+                                            w_post=t["w_post"], gate=t["gate"])
+    torch.cuda.synchronize()
+    for _ in range(3):
+        f = pq.qcast_norm_per_token(t["h"], t["w_pre"], t["y"], t["w_post"], t["gate"], ckpt_fmt="e4m3", stream=side)
+        b = pq.qcast_norm_backward_per_token(t["dy"], f.h_ckpt, f.rstd_pre, t["w_pre"], saved_h_sf=f.h_ckpt_sf,
+                                             saved_y=f.y_ckpt, saved_y_sf=f.y_ckpt_sf, rstd_post=f.rstd_post,
+                                             w_post=t["w_post"], gate=t["gate"], stream=side)
+        side.synchronize()
+        for x, y in list(zip(f, ref)) + list(zip(b, refb)):
+            assert x is None and y is None or torch.equal(x.reshape(-1).view(torch.uint8), y.reshape(-1).view(torch.uint8))
+    # the default stream by its handle, while another one is current
+    with torch.cuda.stream(side):
+        z, zsf = pq.qcast_recast_per_channel_T(ref.out, ref.out_sf, stream=torch.cuda.default_stream(dev))
+    torch.cuda.synchronize()
+    r, rsf = pq.qcast_recast_per_channel_T(ref.out, ref.out_sf)
+    assert torch.equal(z.view(torch.uint8), r.view(torch.uint8)) and torch.equal(zsf, rsf)
+
+
+def test_two_threads_two_streams(dev):
+    ts = [inputs(dev, rows=200 + 57 * i, seed=5 + i) for i in range(2)]
+    alone = [bits(step(t)) for t in ts]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream(dev)
+            with torch.cuda.stream(s):
+                for _ in range(8):
+                    got[i].append(bits(step(ts[i])))
+            s.synchronize()
+        except Exception as e:  # reported on the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(timeout=100)
+    assert not errors, errors
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 8
+        for o in got[i]:
+            assert all(torch.equal(o[k], alone[i][k]) for k in alone[i])
+
+
+def test_step_captured_and_replayed(dev):
+    t = inputs(dev)
+    ref = bits(step(t))
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        step(t)
+    torch.cuda.current_stream(dev).wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):                      # two graphs: neither may use the other's workspaces
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(t)
+        graphs.append((g, out))
+    for replay in range(4):
+        for _, out in graphs:
+            for x in out.values():
+                if x is not None:
+                    x.reshape(-1).view(torch.uint8).fill_(0x40 + replay)
+        # an output poisoned between replays is written again by the replay
+        if replay % 2:
+            streams = [torch.cuda.Stream(dev) for _ in graphs]
+            for s, (g, _) in zip(streams, graphs):
+                s.wait_stream(torch.cuda.current_stream(dev))
+                with torch.cuda.stream(s):
+                    g.replay()
+            for s in streams:
+                torch.cuda.current_stream(dev).wait_stream(s)
+        else:
+            for g, _ in graphs:
+                g.replay()
+        eager = bits(step(t))
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            for k, x in bits(out).items():
+                assert torch.equal(x, ref[k]), (replay, k)
+        assert all(torch.equal(eager[k], ref[k]) for k in ref)
+
+
+class Guarded:
+    def __init__(self, dev):
+        self.dev, self.bufs = dev, []
+
+    def make(self, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((GUARD + n + GUARD,), POISON, dtype=torch.uint8, device=self.dev)
+        self.bufs.append((buf, n))
+        return buf[GUARD:GUARD + n].view(dtype).view(shape)
+
+    def check(self, what):
+        torch.cuda.synchronize()
+        for i, (buf, n) in enumerate(self.bufs):
+            assert (buf[:GUARD] == POISON).all() and (buf[GUARD + n:] == POISON).all(), f"{what}: buffer {i}"
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 384), (129, 256), (300, 1024)])
+def test_nothing_is_written_outside_the_outputs(dev, rows, cols):
+    from precision_quantization_amd import _lib
+    lib = _lib.load()
+    g = Guarded(dev)
+    gen = torch.Generator().manual_seed(rows)
+    f8, f32, b16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    sh = torch.cuda.current_stream(dev).cuda_stream
+    rows_t = (rows + 127) // 128 * 128
+    hh, dv = br.bf16(gen, rows, 2 * cols).to(dev), br.bf16(gen, rows, cols).to(dev)
+    w = torch.rand(rows, generator=gen).to(dev)
+    ck, cks = g.make((rows, 2 * cols), f8), g.make((rows, 2 * cols // 128), f32)
+    pq.qcast_swiglu_checkpoint(hh, w, out=g.make((rows, cols), f8), out_sf=g.make((rows, cols // 128), f32), ckpt=ck, ckpt_sf=cks)
+    g.check("checkpoint")
+    p = lambda shape, dtype: g.make(shape, dtype).data_ptr()
+    nct = cols // 128
+    assert lib.qcast_swiglu_backward_checkpoint(
+        ck.data_ptr(), cks.data_ptr(), dv.data_ptr(), rows, cols, w.data_ptr(), 1, 1, 128, 0.0, 0, 2.0, p((rows, 2 * cols), f8),
+        p((rows, 2 * nct), f32), p((2 * cols, rows_t), f8), p((2 * cols, rows_t // 128), f32), p((cols, rows_t), f8),
+        p((cols, rows_t // 128), f32), p((rows,), f32), p((rows * nct,), f32), sh) == 0
+    g.check("backward")
+    pq.qcast_recast_per_channel_T(ck, cks, out=g.make((2 * cols, rows_t), f8), out_sf=g.make((2 * cols, rows_t // 128), f32))
+    g.check("recast")
+    wv = br.bf16(gen, cols).to(dev)
+    h, y = br.bf16(gen, rows, cols).to(dev), br.bf16(gen, rows, cols).to(dev)
+    r1, r2 = g.make((rows,), f32), g.make((rows,), f32)
+    hc, hcs, yc, ycs = (g.make(s, d) for s, d in (((rows, cols), f8), ((rows, nct), f32)) * 2)
+    assert lib.qcast_norm_per_token(y.data_ptr(), h.data_ptr(), rows, cols, wv.data_ptr(), wv.data_ptr(), wv.data_ptr(), 1, 1.0, 0.0,
+                                    1e-6, 1, 128, 0.0, 2, p((rows, cols), b16), p((rows, cols), f8),
+                                    p((nct, (rows + 3) // 4 * 4), f32), p((rows, cols), b16), r1.data_ptr(), r2.data_ptr(), 1,
+                                    yc.data_ptr(), ycs.data_ptr(), hc.data_ptr(), hcs.data_ptr(), sh) == 0
+    g.check("norm")
+    assert lib.qcast_norm_backward_per_token(
+        h.data_ptr(), y.data_ptr(), rows, cols, 1, hc.data_ptr(), hcs.data_ptr(), yc.data_ptr(), ycs.data_ptr(), r1.data_ptr(),
+        r2.data_ptr(), wv.data_ptr(), wv.data_ptr(), y.data_ptr(), 3, 1.0, 0.0, 1, 128, 0.0, 0, p((rows, cols), b16),
+        p((rows, cols), f8), p((rows, nct), f32), p((rows, cols), b16), p((cols,), f32), p((cols,), f32), p((rows, cols), b16),
+        p((min(rows, pq.NORM_WS_ROWS) * 2 * cols,), f32), sh) == 0
+    g.check("norm backward")

@@ -525,7 +525,7 @@ QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, i
                                    void* stream);
 
 /* Rows of partial sums of qcast_norm_backward_per_token's workspace. */
-#define QCAST_NORM_WS_ROWS 512
+#define QCAST_NORM_WS_ROWS 256
 
 /*
  * Gradient of qcast_norm_per_token, fused with the per-token cast of the

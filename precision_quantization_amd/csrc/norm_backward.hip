@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr int kJoinWaves = 16;     // waves of the joining workgroup
+constexpr int kJoinAhead = 16;     // parts a lane loads at once
 
 // The lane's raw data of one chunk of one row: bf16 octets, or 8-bit codes in
 // the low two words with their scales.
@@ -276,8 +277,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void norm_backward_join_kernel(Nor
   const float* ws = p.ws + (int64_t)blockIdx.y * cols + col;
   float s = 0.0f;
   if (col < cols) {
-#pragma unroll 8
-    for (uint32_t i = wave; i < parts; i += kJoinWaves) s += ws[(int64_t)i * 2 * cols];
+    for (uint32_t i0 = wave; i0 < parts; i0 += kJoinWaves * kJoinAhead) {
+      float v[kJoinAhead];                // all loads in flight before the first sum
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) {
+        const uint32_t j = i0 + i * kJoinWaves;
+        v[i] = j < parts ? ws[(int64_t)j * 2 * cols] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) s += v[i];
+    }
   }
   part[wave][lane] = s;
   __syncthreads();

@@ -166,7 +166,7 @@ int device_ok() {
 }
 
 static_assert(QCAST_NORM_MAX_COLS == 8 * qcast::kNormMaxChunks, "longest row of the norms");
-static_assert(QCAST_NORM_WS_ROWS >= qcast::kNormParts, "workspace rows of the norms");
+static_assert(QCAST_NORM_WS_ROWS == qcast::kNormParts, "workspace rows of the norms");
 
 // The scalar arguments of the norm entry points; `saved_fmt` is the format
 // of 8-bit checkpoints, 0 for none.

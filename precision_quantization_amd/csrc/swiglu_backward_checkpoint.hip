@@ -277,15 +277,23 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   if (p.v.qT) store_tile_rows<kBlock, true>(tile[2], p.v.qT, c0, kTile, gt, rows_T);
 }
 
+constexpr uint32_t kJoin = 16;
+
 // dw[r] = sum over the channel tiles of their partial sums, in tile order.
 __global__ __launch_bounds__(64) void row_weight_join_kernel(const float* __restrict__ ws,
                                                                    uint32_t rows, uint32_t nct,
                                                                    float* __restrict__ dw) {
   const uint32_t r = blockIdx.x * 64 + threadIdx.x;
   if (r >= rows) return;
-  float s = ws[r];
-#pragma unroll 16
-  for (uint32_t i = 1; i < nct; ++i) s += ws[(uint64_t)i * rows + r];
+  float s = 0.0f;
+  for (uint32_t i0 = 0; i0 < nct; i0 += kJoin) {
+    float v[kJoin];                       // all loads in flight before the first sum
+#pragma unroll
+    for (uint32_t i = 0; i < kJoin; ++i)
+      v[i] = i0 + i < nct ? ws[(uint64_t)(i0 + i) * rows + r] : 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < kJoin; ++i) s += v[i];
+  }
   dw[r] = s;
 }
 

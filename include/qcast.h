@@ -524,8 +524,18 @@ QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, i
                                    float* y_ckpt_sf, void* h_ckpt, float* h_ckpt_sf,
                                    void* stream);
 
-/* Rows of partial sums of qcast_norm_backward_per_token's workspace. */
-#define QCAST_NORM_WS_ROWS 256
+/* Rows of partial column sums that qcast_norm_backward_per_token writes to its
+ * workspace: one per workgroup, and as many workgroups as 256 compute units
+ * run at once (16 waves each, a wave for 512 columns), but 256 or at least 8
+ * rows each. It follows from the sizes alone, and so does the order of the
+ * sums. */
+static inline int64_t qcast_norm_ws_rows(int64_t rows, int64_t cols) {
+  const int64_t waves = (cols + 511) / 512;
+  const int64_t most = waves > 0 && waves < 16 ? 256 * (16 / waves) : 256;
+  int64_t n = rows / 8 < most ? rows / 8 : most;
+  if (n < 256) n = 256;
+  return n < rows ? n : rows;
+}
 
 /*
  * Gradient of qcast_norm_per_token, fused with the per-token cast of the
@@ -552,7 +562,7 @@ QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, i
  *            least one of q (with sf) and dy_out is given.
  *   dw_pre, dw_post  [cols] fp32; dgate [cols] fp32, [rows] fp32 or [rows,
  *            cols] bf16 by gate_kind. Each may be NULL; all are overwritten.
- *   ws       min(rows, QCAST_NORM_WS_ROWS) * 2 * cols * 4 bytes of device
+ *   ws       qcast_norm_ws_rows(rows, cols) * 2 * cols * 4 bytes of device
  *            memory (16-byte aligned; no particular contents) that no other
  *            call uses at the same time; may be NULL when rows is 0.
  *   Everything else as qcast_norm_per_token.

@@ -24,7 +24,7 @@ from contextlib import nullcontext
 import torch
 
 from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E5M2, FMT_E5M6, GATE_CHANNEL, GATE_FULL, GATE_NONE,
-                   GATE_TOKEN, NORM_WS_ROWS, OUT_BF16, OUT_F32, SF_COL_MAJOR, SF_PACKED_UE8M0,
+                   GATE_TOKEN, OUT_BF16, OUT_F32, SF_COL_MAJOR, SF_PACKED_UE8M0,
                    SF_ROUND_POW2, QcastError, check, fmt_id, load)
 
 __all__ = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per_block",
@@ -753,6 +753,14 @@ def qcast_norm_per_token(h, w_pre, y=None, w_post=None, gate=None, residual_scal
     return NormOut(h_out, out, out_sf, x, r1, r2, yc, yc_sf, hc, hc_sf)
 
 
+def norm_ws_rows(rows, cols):
+    """Rows of partial sums of the norm backward's workspace
+    (``qcast_norm_ws_rows`` of include/qcast.h)."""
+    waves = (cols + 511) // 512
+    most = 256 * (16 // waves) if 0 < waves < 16 else 256
+    return min(rows, max(256, min(most, rows // 8)))
+
+
 def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h_sf=None,
                                   saved_y=None, saved_y_sf=None, rstd_post=None, w_post=None,
                                   gate=None, residual_scale=1.0, weight_offset=0.0, fmt="e4m3",
@@ -814,7 +822,7 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
         if kind:
             dgate = torch.empty(gate.shape, dtype=bf16 if kind == GATE_FULL else f32, device=dev)
         if rows:
-            ws = torch.empty(min(rows, NORM_WS_ROWS) * 2 * cols, dtype=f32, device=dev)
+            ws = torch.empty(norm_ws_rows(rows, cols) * 2 * cols, dtype=f32, device=dev)
         check(load().qcast_norm_backward_per_token(
             dx.data_ptr(), dhptr, rows, cols, sf, shptr, shsf, syptr, sysf, r1ptr, r2ptr, wpptr,
             wqptr, gptr, kind, residual_scale, weight_offset, f, group, clamp_min, sf_flags,

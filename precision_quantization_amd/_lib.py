@@ -22,7 +22,6 @@ GATE_NONE = 0
 GATE_CHANNEL = 1
 GATE_TOKEN = 2
 GATE_FULL = 3
-NORM_WS_ROWS = 256          # QCAST_NORM_WS_ROWS
 _FMT = {"e4m3": FMT_E4M3, "e2m1": FMT_E2M1, "e5m2": FMT_E5M2, "e5m6": FMT_E5M6}
 
 _lib = None

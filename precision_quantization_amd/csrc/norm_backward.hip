@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr int kJoinWaves = 16;     // waves of the joining workgroup
-constexpr int kJoinAhead = 16;     // parts a lane loads at once
+constexpr int kJoinAhead = 8;      // parts a lane loads at once
 
 // The lane's raw data of one chunk of one row: bf16 octets, or 8-bit codes in
 // the low two words with their scales.
@@ -320,15 +320,10 @@ auto pick_saved(const NormBackward& p) {
 
 }  // namespace
 
-// Workgroups of the pass: one per row up to kNormParts.
-uint32_t norm_backward_parts(int64_t rows) {
-  return (uint32_t)(rows < kNormParts ? rows : kNormParts);
-}
-
-hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, hipStream_t stream) {
+hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, uint32_t parts,
+                                hipStream_t stream) {
   if (p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
-  const uint32_t parts = norm_backward_parts(rows);
   if (parts) {
     const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
     const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);

@@ -166,7 +166,6 @@ int device_ok() {
 }
 
 static_assert(QCAST_NORM_MAX_COLS == 8 * qcast::kNormMaxChunks, "longest row of the norms");
-static_assert(QCAST_NORM_WS_ROWS == qcast::kNormParts, "workspace rows of the norms");
 
 // The scalar arguments of the norm entry points; `saved_fmt` is the format
 // of 8-bit checkpoints, 0 for none.
@@ -686,7 +685,8 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
   p.offset = weight_offset;
   p.inv_n = 1.0f / (float)cols;
   p.chunks = (uint32_t)(cols / 8);
-  return finish(qcast::launch_norm_backward(p, rows, static_cast<hipStream_t>(stream)));
+  return finish(qcast::launch_norm_backward(p, rows, (uint32_t)qcast_norm_ws_rows(rows, cols),
+                                            static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

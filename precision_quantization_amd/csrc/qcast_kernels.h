@@ -184,7 +184,6 @@ bool tile_fits(int64_t rows, int64_t cols, int64_t stride);
 // The norms around a block (norm.hip, norm_backward.hip).
 enum GateKind : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
 constexpr uint32_t kNormMaxChunks = 4096;      // 32768 columns: 1024 threads x 4 chunks of 8
-constexpr int64_t kNormParts = 256;            // workgroups of the backward pass
 
 struct NormForward {
   const uint16_t* y;         // or null
@@ -220,7 +219,7 @@ struct NormBackward {
   uint16_t* dy_out;          // or null
   float* sums[3];            // dw_pre, dw_post, dgate of a channel gate; each may be null
   void* dgate;               // of a token or full gate, or null
-  float* ws;                 // [min(rows, kNormParts)][2][cols]
+  float* ws;                 // [parts][2][cols]
   RowCast cast;
   int saved_fmt;             // 0: bf16
   int gate_kind;
@@ -228,6 +227,8 @@ struct NormBackward {
   float inv_n;               // 1 / cols
   uint32_t chunks;
 };
-hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, hipStream_t stream);
+// parts: workgroups that walk the rows (at most rows)
+hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, uint32_t parts,
+                                hipStream_t stream);
 
 }  // namespace qcast

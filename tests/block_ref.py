@@ -193,7 +193,10 @@ def norm_backward_slack(dx, dh_in, h, r2, w_pre, y=None, r1=None, w_post=None, g
     mean1 = (g * xh).sum(1, keepdim=True) / n
     size_d = di + r2[:, None] * (g + xh * mean1)
     d = U * (10 * size_d + (ROW_SUM + 4) * r2[:, None] * xh * mean1)
-    steps = U * (rows // 512 + 16 + 32 + 8)
+    # a column sum: a workgroup's rows one after another (at least 256 workgroups
+    # share them, or each row has its own), then a wave's 16th of at most 4096
+    # workgroups, the 16 waves, and the products
+    steps = U * (rows // 256 + 256 + 16 + 8)
     out = dict(dh=alpha * d, dw_pre=(steps * dx.abs() * xh).sum(0))
     if y is None:
         return out

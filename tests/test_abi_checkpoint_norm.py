@@ -184,3 +184,20 @@ def test_binding_refuses_cpu_tensors():
                  lambda: pq.qcast_norm_backward_per_token(x, x, sf, w)):
         with pytest.raises(pq.QcastError):
             call()
+
+
+def test_workspace_rows_of_header_and_binding(tmp_path):
+    import os
+    import subprocess
+
+    import precision_quantization_amd as pq
+    from conftest import ROOT
+    sizes = [(r, c) for r in (0, 1, 255, 256, 257, 2047, 2048, 2056, 8192, 16384, 40000) for c in (32, 512, 544, 1024, 7168, 8192, 32768)]
+    src = tmp_path / "ws.c"
+    src.write_text('#include <stdio.h>\n#include "qcast.h"\nint main(void) {\n' +
+                   "".join(f'  printf("%lld\\n", (long long)qcast_norm_ws_rows({r}, {c}));\n' for r, c in sizes) + "  return 0;\n}\n")
+    exe = str(tmp_path / "ws")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", f"-I{os.path.join(ROOT, 'include')}", str(src), "-o", exe], check=True)
+    got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [pq.norm_ws_rows(r, c) for r, c in sizes]
+    assert pq.norm_ws_rows(8192, 2048) == 1024 and pq.norm_ws_rows(4096, 7168) == 256 and pq.norm_ws_rows(3, 512) == 3

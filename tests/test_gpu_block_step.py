@@ -224,7 +224,7 @@ class Guarded:
             assert (buf[:GUARD] == POISON).all() and (buf[GUARD + n:] == POISON).all(), f"{what}: buffer {i}"
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 384), (129, 256), (300, 1024)])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 384), (129, 256), (300, 1024), (2500, 128)])
 def test_nothing_is_written_outside_the_outputs(dev, rows, cols):
     from precision_quantization_amd import _lib
     lib = _lib.load()
@@ -260,5 +260,5 @@ def test_nothing_is_written_outside_the_outputs(dev, rows, cols):
         h.data_ptr(), y.data_ptr(), rows, cols, 1, hc.data_ptr(), hcs.data_ptr(), yc.data_ptr(), ycs.data_ptr(), r1.data_ptr(),
         r2.data_ptr(), wv.data_ptr(), wv.data_ptr(), y.data_ptr(), 3, 1.0, 0.0, 1, 128, 0.0, 0, p((rows, cols), b16),
         p((rows, cols), f8), p((rows, nct), f32), p((rows, cols), b16), p((cols,), f32), p((cols,), f32), p((rows, cols), b16),
-        p((min(rows, pq.NORM_WS_ROWS) * 2 * cols,), f32), sh) == 0
+        p((pq.norm_ws_rows(rows, cols) * 2 * cols,), f32), sh) == 0
     g.check("norm backward")

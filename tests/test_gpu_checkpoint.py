@@ -191,3 +191,37 @@ def test_empty(dev):
     t, tsf = pq.qcast_recast_per_channel_T(q, torch.zeros(0, 2, device=dev))
     assert t.shape == (256, 0) and tsf.shape == (256, 0)
     assert pq.qcast_swiglu_checkpoint(torch.zeros(0, 256, dtype=torch.bfloat16, device=dev))[2].shape == (0, 256)
+
+
+def test_swiglu_checkpoint_past_one_launch(dev):
+    # more than 2^24 chunks of 8: the rows are cast in two launches
+    rows, cols = 65600, 2048
+    g = torch.Generator(device=dev).manual_seed(1)
+    h = (torch.randn(rows, 2 * cols, generator=g, device=dev) * 2).to(torch.bfloat16)
+    w = torch.rand(rows, generator=g, device=dev)
+    q, sf, c, csf = pq.qcast_swiglu_checkpoint(h, w, sf_flags=COL)
+    q2, sf2 = pq.qcast_swiglu_per_token_sf(h, w, sf_flags=COL)
+    c2, csf2 = pq.qcast_per_token(h)
+    torch.cuda.synchronize()
+    for a, b in ((q, q2), (sf, sf2), (c, c2), (csf, csf2)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_recast_of_very_many_rows(dev):
+    # near the longest transposed row; offsets pass 2^31 bytes
+    rows, cols = (1 << 24) - 256 - 5, 160
+    g = torch.Generator(device=dev).manual_seed(2)
+    q = torch.randint(0, 256, (rows, cols), generator=g, device=dev, dtype=torch.uint8)
+    q = torch.where((q & 0x7F) == 0x7F, q ^ 1, q).view(torch.float8_e4m3fn)     # no NaN codes
+    sf = torch.rand(rows, cols // 32, generator=g, device=dev) + 0.5
+    out, out_sf = pq.qcast_recast_per_channel_T(q, sf)
+    torch.cuda.synchronize()
+    rows_t = (rows + 127) // 128 * 128
+    assert out.shape == (cols, rows_t) and not out.view(torch.uint8)[:, rows:].any()
+    for a in (0, 128 * 1000, 128 * 65536, rows_t - 128):
+        b = min(rows, a + 128)
+        x = q[a:b].float() * sf[a:b].repeat_interleave(32, 1)
+        xt = torch.cat([x, x.new_zeros(128 - (b - a), cols)]).t().contiguous().cpu().numpy()
+        qr, sfr = oracle.per_token_f32(xt, "e4m3", 128)
+        assert np.array_equal(br.raw(out[:, a:a + 128].contiguous()), qr)
+        assert np.array_equal(br.raw(out_sf[:, a // 128:a // 128 + 1].contiguous()), sfr)

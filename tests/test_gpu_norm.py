@@ -248,3 +248,44 @@ def test_refusals_of_the_binding(dev):
                dict(saved_h_sf=sf, saved_y=q), dict(saved_h_sf=sf, saved_y=x.to(torch.float8_e5m2), saved_y_sf=sf)):
         with pytest.raises(pq.QcastError):
             pq.qcast_norm_backward_per_token(x, q, r, w, **kw)
+
+
+def test_one_checkpoint_of_two_through_the_c_abi(dev):
+    from precision_quantization_amd import _lib
+    lib = _lib.load()
+    v, _ = inputs(37, 512, None, True, 8)
+    h, y, w = (v[k].to(dev) for k in ("h", "y", "w_pre"))
+    full = pq.qcast_norm_per_token(h, w, y, w, ckpt_fmt="e5m2")
+    sh = torch.cuda.current_stream(dev).cuda_stream
+    for which in ("y", "h"):
+        ho = torch.empty_like(h)
+        x = torch.empty_like(h)
+        c = torch.zeros(37, 512, dtype=torch.uint8, device=dev)
+        s = torch.zeros(37, 4, device=dev)
+        own = (c.data_ptr(), s.data_ptr())
+        args = own + (None, None) if which == "y" else (None, None) + own
+        # no codes of x, no factors: x in bf16 and one checkpoint
+        assert lib.qcast_norm_per_token(y.data_ptr(), h.data_ptr(), 37, 512, w.data_ptr(), w.data_ptr(), None, 0, 1.0, 0.0, 1e-6, 1,
+                                        128, 0.0, 0, ho.data_ptr(), None, None, x.data_ptr(), None, None, 3, *args, sh) == 0
+        torch.cuda.synchronize()
+        want = (full.y_ckpt, full.y_ckpt_sf) if which == "y" else (full.h_ckpt, full.h_ckpt_sf)
+        assert same(c, want[0]) and same(s, want[1]) and same(ho, full.h)
+
+
+def test_rows_of_more_than_2_31_bytes(dev):
+    # offsets past 31 bits, first and last rows against a call on those rows
+    rows, cols = 150000, 7168
+    g = torch.Generator(device=dev).manual_seed(3)
+    h = torch.randn(rows, cols, generator=g, device=dev, dtype=torch.bfloat16)
+    w = torch.randn(cols, generator=g, device=dev).to(torch.bfloat16)
+    a = pq.qcast_norm_per_token(h, w, h, w, ckpt_fmt="e4m3")
+    b = pq.qcast_norm_backward_per_token(h, a.h_ckpt, a.rstd_pre, w, dh=h, saved_h_sf=a.h_ckpt_sf, saved_y=a.y_ckpt,
+                                         saved_y_sf=a.y_ckpt_sf, rstd_post=a.rstd_post, w_post=w)
+    for sl in (slice(0, 3), slice(rows - 3, rows)):
+        t = h[sl].contiguous()
+        c = pq.qcast_norm_per_token(t, w, t, w, ckpt_fmt="e4m3")
+        d = pq.qcast_norm_backward_per_token(t, c.h_ckpt, c.rstd_pre, w, dh=t, saved_h_sf=c.h_ckpt_sf, saved_y=c.y_ckpt,
+                                             saved_y_sf=c.y_ckpt_sf, rstd_post=c.rstd_post, w_post=w)
+        for x, y in list(zip(a, c)) + [(b.dh, d.dh), (b.out, d.out), (b.out_sf, d.out_sf)]:
+            if x is not None:
+                assert same(x[sl].contiguous(), y)

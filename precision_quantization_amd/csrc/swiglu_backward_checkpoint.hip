@@ -154,6 +154,9 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   const uint8_t* cp = p.ckpt + (uint64_t)tq * 2 * cols + c0 + ch * 8;
   const uint16_t* dp = p.dv + (uint64_t)tq * cols + c0 + ch * 8;
   const float* sp = p.ckpt_sf + (uint64_t)tq * gpr + ct;
+  // plain loads: 32 us where the inputs are in the Infinity Cache (a gradient
+  // that the product before has just written) against 41 with streaming
+  // loads, and no slower from HBM (40.6 against 41.3; 8192 x 2048)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     graw[i] = uraw[i] = u32x2{0u, 0u};
@@ -161,9 +164,9 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
     gsf[i] = usf[i] = 0.0f;
     wr[i] = 1.0f;
     if (i < left) {
-      graw[i] = load_stream(reinterpret_cast<const u32x2*>(cp + i * 2 * cols));
-      uraw[i] = load_stream(reinterpret_cast<const u32x2*>(cp + i * 2 * cols + cols));
-      draw[i] = load_stream(reinterpret_cast<const u32x4*>(dp + i * cols));
+      graw[i] = *reinterpret_cast<const u32x2*>(cp + i * 2 * cols);
+      uraw[i] = *reinterpret_cast<const u32x2*>(cp + i * 2 * cols + cols);
+      draw[i] = *reinterpret_cast<const u32x4*>(dp + i * cols);
       gsf[i] = sp[i * gpr];
       usf[i] = sp[i * gpr + gpr / 2];
       if (p.w) wr[i] = p.w[tq + i];

@@ -62,8 +62,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_checkpoint_kernel(
   const uint32_t jc = c - row * chunks_per_row;
   const uint32_t hc = row * 2 * chunks_per_row + jc;
   const u32x4* src = reinterpret_cast<const u32x4*>(h) + hc;
-  const u32x4 graw = load_stream(src);
-  const u32x4 uraw = load_stream(src + chunks_per_row);
+  // plain loads: h was just written by a product, and what of it is in the
+  // Infinity Cache is read from there (20.2 against 22.0 us, 8192 x 2048)
+  const u32x4 graw = src[0];
+  const u32x4 uraw = src[chunks_per_row];
   const float wr = w ? w[row] : 1.0f;
 
   float* crow = ckpt_sf + hc / kLanes;

@@ -482,7 +482,7 @@ typedef enum {
 } qcast_gate_kind;
 
 /* Longest row of the norm entry points. */
-#define QCAST_NORM_MAX_COLS 32768
+#define QCAST_NORM_MAX_COLS 16384
 
 /*
  * The norm after a block, its gate and the scaled residual, the norm before

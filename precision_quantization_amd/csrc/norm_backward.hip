@@ -29,13 +29,21 @@
 // dw_post = gate * T, dgate = wp * T. With one chunk of 8 columns per lane
 // (rows of up to 8192) the next row is loaded while the current one is
 // worked on, and the values of the first half are kept for the second; longer
-// rows keep the packed inputs and form the values again.
+// rows (up to 16384) keep the packed inputs, form the values again, and hold
+// the column sums in LDS (128 KB, each lane its own words).
+//
+// What it must move: dx, dh', both saved tensors, dh and the codes of dy (9
+// bytes per element from 8-bit checkpoints, 11 from bf16), plus 8 bytes per
+// column and workgroup of partial sums. 4096 x 7168, channel gate, from
+// checkpoints: 59 us, of which the join takes 5 (a copy of 264 MB: 42).
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
 
 namespace qcast {
 namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxWaves = 16;
 constexpr int kJoinWaves = 16;     // waves of the joining workgroup
@@ -139,6 +147,17 @@ __device__ __forceinline__ Values chunk_values(const Chunk& ch, const float q[8]
   return v;
 }
 
+// A lane's 8 column sums in two LDS rows of one f32x4 per thread.
+__device__ __forceinline__ void load_sums(const f32x4* row, float v[8]) {
+  const f32x4 a = row[threadIdx.x], b = row[1024 + threadIdx.x];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store_sums(f32x4* row, const float v[8]) {
+  row[threadIdx.x] = f32x4{v[0], v[1], v[2], v[3]};
+  row[1024 + threadIdx.x] = f32x4{v[4], v[5], v[6], v[7]};
+}
+
 // kSaved: 0 for bf16, else the format of the 8-bit checkpoints. kGate:
 // kGateFull, kGateToken, or kGateNone for both other kinds (a channel gate is
 // one of the column factors). kY: there is a block output.
@@ -148,13 +167,16 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
   __shared__ __attribute__((aligned(16))) float part[2][kMaxWaves][4];
   const uint32_t chunks = p.chunks;
   constexpr bool kFull = kGate == kGateFull;
-  float q[kC][8], c[kC][8], s_pre[kC][8], s_post[kC][8];
+  // the lane's column sums: registers, or (kC == 2) its own LDS words
+  __shared__ __attribute__((aligned(16))) f32x4 acc[kKeep ? 1 : 4 * kC * 1024];
+  float q[kC][8], c[kC][8], s_pre[8], s_post[8];
 #pragma unroll
-  for (int k = 0; k < kC; ++k) {
-    const uint32_t jc = threadIdx.x + k * blockDim.x;
-    if (kKeep) column_factors(p, jc, jc < chunks, q[k], c[k]);
+  for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = 0.0f;
+  if constexpr (kKeep) {
+    column_factors(p, threadIdx.x, threadIdx.x < chunks, q[0], c[0]);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[k][i] = s_post[k][i] = 0.0f;
+    for (int i = 0; i < 4 * kC; ++i) acc[i * 1024 + threadIdx.x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   Chunk next;
   if (kKeep)
@@ -183,17 +205,19 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
       if (!kKeep) column_factors(p, jc, jc < chunks, q[k], c[k]);
       float dx[8];
       const Values v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx);
+      if constexpr (!kKeep) load_sums(acc + 4 * k * 1024, s_pre);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s1 = __builtin_fmaf(v.gx[i], v.x[i], s1);
-        s_pre[k][i] = __builtin_fmaf(dx[i], v.x[i], s_pre[k][i]);
+        s_pre[i] = __builtin_fmaf(dx[i], v.x[i], s_pre[i]);
         if (kY) {
           const float cc = v.a[i] * v.c[i];
           s2 = __builtin_fmaf(__builtin_fmaf(r2, v.gx[i], v.dh[i]), cc, s2);
           s3 = __builtin_fmaf(v.x[i], cc, s3);
         }
       }
-      if (kKeep) kept = v;
+      if constexpr (kKeep) kept = v;
+      else store_sums(acc + 4 * k * 1024, s_pre);
     }
     block_sum3(s1, s2, s3, part[parity]);
     const float m1 = s1 * p.inv_n;
@@ -223,14 +247,16 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
       if (jc < chunks)
         store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, pack8_bf16(out));
       if (kY) {
+        if constexpr (!kKeep) load_sums(acc + (4 * k + 2) * 1024, s_post);
         // without the column's own factors: d * a * (token or elementwise gate)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float dz = kFull ? d[i] * g[i] : kGate == kGateToken ? d[i] * row_gate : d[i];
-          s_post[k][i] = __builtin_fmaf(dz, v.a[i], s_post[k][i]);
+          s_post[i] = __builtin_fmaf(dz, v.a[i], s_post[i]);
           out[i] = dz * (kFull ? c[k][i] : v.c[i]);
           if (p.w_post) out[i] = r1 * __builtin_fmaf(-v.a[i], m2, out[i]);
         }
+        if constexpr (!kKeep) store_sums(acc + (4 * k + 2) * 1024, s_post);
         if (jc < chunks) {
           if (kFull && p.dgate) {
             float dg[8];
@@ -249,15 +275,17 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
   for (int k = 0; k < kC; ++k) {
     const uint32_t jc = threadIdx.x + k * blockDim.x;
     if (jc < chunks) {
+      if constexpr (!kKeep) {
+        load_sums(acc + 4 * k * 1024, s_pre);
+        load_sums(acc + (4 * k + 2) * 1024, s_post);
+      }
       float* o = p.ws + (int64_t)blockIdx.x * 2 * 8 * chunks + 8 * jc;
-      typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<f32x4*>(o + i) =
-            f32x4{s_pre[k][i], s_pre[k][i + 1], s_pre[k][i + 2], s_pre[k][i + 3]};
+        *reinterpret_cast<f32x4*>(o + i) = f32x4{s_pre[i], s_pre[i + 1], s_pre[i + 2], s_pre[i + 3]};
         if (kY)
           *reinterpret_cast<f32x4*>(o + 8 * chunks + i) =
-              f32x4{s_post[k][i], s_post[k][i + 1], s_post[k][i + 2], s_post[k][i + 3]};
+              f32x4{s_post[i], s_post[i + 1], s_post[i + 2], s_post[i + 3]};
       }
     }
   }
@@ -325,9 +353,9 @@ hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, uint32_t pa
   if (p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
   if (parts) {
-    const int kc = p.chunks > 2048 ? 4 : p.chunks > 1024 ? 2 : 1;
+    const int kc = p.chunks > 1024 ? 2 : 1;
     const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
-    auto kernel = kc == 1 ? pick_saved<1>(p) : kc == 2 ? pick_saved<2>(p) : pick_saved<4>(p);
+    auto kernel = kc == 1 ? pick_saved<1>(p) : pick_saved<2>(p);
     launch_kernel(kernel, dim3(parts), dim3(threads), 0, stream, p, (uint32_t)rows);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;

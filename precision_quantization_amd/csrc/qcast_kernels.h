@@ -183,7 +183,7 @@ bool tile_fits(int64_t rows, int64_t cols, int64_t stride);
 
 // The norms around a block (norm.hip, norm_backward.hip).
 enum GateKind : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
-constexpr uint32_t kNormMaxChunks = 4096;      // 32768 columns: 1024 threads x 4 chunks of 8
+constexpr uint32_t kNormMaxChunks = 2048;      // 16384 columns: 1024 threads x 2 chunks of 8
 
 struct NormForward {
   const uint16_t* y;         // or null

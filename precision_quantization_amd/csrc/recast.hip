@@ -21,10 +21,8 @@
 namespace qcast {
 namespace {
 
-#ifndef QCAST_RC_STRIP
-#define QCAST_RC_STRIP 2
-#endif
-constexpr uint32_t kStrip = QCAST_RC_STRIP;
+// channel tiles per strip: 52.5 us against 53.8 with 1 and 53.4 with 4
+constexpr uint32_t kStrip = 2;
 
 // The fp32 value of code j (0..15) of a token's 16 codes.
 template <int kIn>

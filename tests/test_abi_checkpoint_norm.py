@@ -106,7 +106,7 @@ NO_Y = dict(y=None, w_post=None, gate=None, kind=0, h_out=None, rstd_post=None, 
 def test_norm(lib):
     assert norm(lib, fmt=9) == norm(lib, cf=E2M1) == norm(lib, flags=8) == ERR_FORMAT
     assert norm(lib, group=16) == ERR_GROUP
-    assert norm(lib, cols=200) == norm(lib, rows=-1) == norm(lib, cols=32768 + 128) == ERR_SHAPE
+    assert norm(lib, cols=200) == norm(lib, rows=-1) == norm(lib, cols=16384 + 128) == ERR_SHAPE
     assert norm(lib, cols=64, group=32) == ERR_SHAPE          # checkpoints take groups of 128
     assert norm(lib, rows=1 << 31, cols=128) == norm(lib, cols=384, flags=4) == ERR_SHAPE
     for bad in (dict(eps=NAN), dict(eps=-1.0), dict(eps=INF), dict(alpha=INF), dict(offset=NAN),
@@ -145,7 +145,7 @@ def nbwd(lib, dx=A, dh_in=A, rows=4, cols=256, saved=E4M3, h=A, h_sf=A, y=A, y_s
 def test_norm_backward(lib):
     assert nbwd(lib, fmt=9) == nbwd(lib, saved=E2M1) == nbwd(lib, flags=8) == ERR_FORMAT
     assert nbwd(lib, group=16) == ERR_GROUP
-    assert nbwd(lib, cols=200) == nbwd(lib, rows=-1) == nbwd(lib, cols=32768 + 128) == ERR_SHAPE
+    assert nbwd(lib, cols=200) == nbwd(lib, rows=-1) == nbwd(lib, cols=16384 + 128) == ERR_SHAPE
     assert nbwd(lib, cols=192, group=64) == ERR_SHAPE
     for bad in (dict(alpha=NAN), dict(offset=INF), dict(kind=7), dict(clamp_min=INF)):
         assert nbwd(lib, **bad) == ERR_VALUE, bad
@@ -192,7 +192,7 @@ def test_workspace_rows_of_header_and_binding(tmp_path):
 
     import precision_quantization_amd as pq
     from conftest import ROOT
-    sizes = [(r, c) for r in (0, 1, 255, 256, 257, 2047, 2048, 2056, 8192, 16384, 40000) for c in (32, 512, 544, 1024, 7168, 8192, 32768)]
+    sizes = [(r, c) for r in (0, 1, 255, 256, 257, 2047, 2048, 2056, 8192, 16384, 40000) for c in (32, 512, 544, 1024, 7168, 8192, 16384)]
     src = tmp_path / "ws.c"
     src.write_text('#include <stdio.h>\n#include "qcast.h"\nint main(void) {\n' +
                    "".join(f'  printf("%lld\\n", (long long)qcast_norm_ws_rows({r}, {c}));\n' for r, c in sizes) + "  return 0;\n}\n")

@@ -45,7 +45,8 @@
  *  - The return value is a qcast_status. Arguments are checked before any
  *    HIP call; on an error nothing is launched and no output is touched.
  *    QCAST_ERR_LAUNCH reports a failed launch (hipGetLastError).
- *  - rows == 0 (or an empty row) is valid and launches nothing.
+ *  - rows == 0 (or an empty row) is valid and launches nothing (but sums
+ *    over no rows that a call returns are written as zeros).
  *  - Shapes past the kernels' 32-bit indexing return QCAST_ERR_SHAPE before
  *    any HIP call: rows * cols / group < 2^31 scale groups for the per-token
  *    casts; for the others, the limits stated with each entry point.

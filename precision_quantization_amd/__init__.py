@@ -14,6 +14,12 @@ with two 12-bit codes per three bytes (a little-endian bit stream), scales as
 rows of its output (``code_shape``): columns for the per-token, SwiGLU,
 per-block and per-channel casts, tokens for the transposed per-channel ones.
 
+Around the products of a training step, the SwiGLU input and the norms' inputs
+can be kept as 8-bit codes (``qcast_swiglu_checkpoint``, ``qcast_norm_per_token``)
+and read by the backward pass (``qcast_swiglu_backward_checkpoint``,
+``qcast_norm_backward_per_token``, ``qcast_recast_per_channel_T``). These calls
+allocate what they return for the stream they run on.
+
 ``per_token_cast(x, fmt='e4m3', num_per_channels=128) -> (out, out_sf)``
 mirrors the call shown in the quick start of the page
 "DeepSeek开源TileKernels：用Python写的GPU算子逼近硬件性能上限".

@@ -197,7 +197,7 @@ def norm_backward_slack(dx, dh_in, h, r2, w_pre, y=None, r1=None, w_post=None, g
     # share them, or each row has its own), then a wave's 16th of at most 4096
     # workgroups, the 16 waves, and the products
     steps = U * (rows // 256 + 256 + 16 + 8)
-    out = dict(dh=alpha * d, dw_pre=(steps * dx.abs() * xh).sum(0))
+    out = dict(dh=abs(alpha) * d, dw_pre=(steps * dx.abs() * xh).sum(0))
     if y is None:
         return out
     a = y.abs() if r1 is None else y.abs() * r1[:, None]

@@ -92,6 +92,22 @@ __device__ __forceinline__ Chunk load_chunk(const NormBackward& p, uint32_t row,
   return c;
 }
 
+// Waits for the loads of a chunk here. Memory operations complete in order, so
+// a wait after the current row's stores would be a wait for those stores too.
+template <int kSaved, int kGate, bool kY>
+__device__ __forceinline__ void arrive(Chunk& c) {
+  asm volatile("" : "+v"(c.dx), "+v"(c.dh), "+v"(c.r2));
+  if constexpr (kSaved != 0) {
+    asm volatile("" : "+v"(c.hs.x), "+v"(c.hs.y), "+v"(c.hsf));
+    if constexpr (kY) asm volatile("" : "+v"(c.ys.x), "+v"(c.ys.y), "+v"(c.ysf));
+  } else {
+    asm volatile("" : "+v"(c.hs));
+    if constexpr (kY) asm volatile("" : "+v"(c.ys));
+  }
+  if constexpr (kY) asm volatile("" : "+v"(c.r1));
+  if constexpr (kGate == kGateToken) asm volatile("" : "+v"(c.row_gate));
+}
+
 template <int kSaved>
 __device__ __forceinline__ void saved_values(const u32x4& raw, float sf, float v[8]) {
   if constexpr (kSaved != 0) {
@@ -244,8 +260,11 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
         out[i] = p.alpha * d[i];
       }
       const int64_t at = (int64_t)row * chunks + jc;
-      if (jc < chunks)
-        store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, pack8_bf16(out));
+      const u32x4 dh_bits = pack8_bf16(out);
+      // 4096 x 7168: 57 us against 62, 8192 x 5120: 77 against 89 (with an
+      // elementwise gate it spills registers: 1000 x 2048 15.7 against 14.1)
+      if constexpr (kKeep && !kFull) arrive<kSaved, kGate, kY>(next);
+      if (jc < chunks) store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, dh_bits);
       if (kY) {
         if constexpr (!kKeep) load_sums(acc + (4 * k + 2) * 1024, s_post);
         // without the column's own factors: d * a * (token or elementwise gate)

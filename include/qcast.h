@@ -512,7 +512,11 @@ typedef enum {
  *            cols/128] scales: the per-token casts (group 128, default floor)
  *            of y and of the fp32 h'. Each pair may be NULL; with neither,
  *            ckpt_fmt is ignored. They need cols % 128 == 0.
- *   eps      finite and >= 0; residual_scale and weight_offset finite.
+ *   eps      finite and >= 0; residual_scale and weight_offset finite. The
+ *            squares are summed in fp32: a mean square + eps of 0 gives an
+ *            infinite factor (and NaN from a row of zeros), a sum past fp32's
+ *            range the factor 0, and one below fp32's normal numbers is not
+ *            held to the accuracy of the rest.
  *   group 32, 64 or 128; cols % group == 0; cols <= QCAST_NORM_MAX_COLS;
  *   rows < 2^31. Every bf16 tensor and code output is 16-byte aligned.
  */

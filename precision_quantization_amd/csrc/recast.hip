@@ -12,7 +12,9 @@
 // consecutive channels (16 bytes) of 4 consecutive tokens and keeps the
 // codes, not the values: they are decoded once for the maxima and again for
 // the codes, which costs one conversion per two values and saves 64
-// registers. 8 lanes cover a token's 128 channels.
+// registers. 8 lanes cover a token's 128 channels. Bound by HBM traffic in
+// 128-byte pieces on both sides: 44 us for 16384 x 7168, 5.5 TB/s (a copy of
+// as many bytes 39; twice the tokens per tile, 256-byte pieces out, 3 us more).
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -20,8 +22,6 @@
 
 namespace qcast {
 namespace {
-
-
 
 // The fp32 value of code j (0..15) of a token's 16 codes.
 template <int kIn>

@@ -694,6 +694,11 @@ def qcast_recast_per_channel_T(q, sf, fmt="e4m3", group=128, clamp_min=0.0, sf_f
     return out, out_sf
 
 
+def _no_empty_rows(rows, cols):
+    if rows and not cols:
+        raise QcastError(2, "there is no norm of rows without columns")
+
+
 def _gate_arg(gate, rows, cols, device):
     """(kind, pointer) of a gate: [cols] bf16, [rows] fp32 or [rows, cols] bf16."""
     if gate is None:
@@ -721,6 +726,7 @@ def qcast_norm_per_token(h, w_pre, y=None, w_post=None, gate=None, residual_scal
     f = fmt_id(fmt)
     h = _bf16_input(h, "h")
     rows, cols = h.shape
+    _no_empty_rows(rows, cols)
     dev = h.device
     bf16, f32 = torch.bfloat16, torch.float32
     wqptr = _like(w_pre, (cols,), bf16, dev, "w_pre")
@@ -785,6 +791,7 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
     f = fmt_id(fmt)
     dx = _bf16_input(dx, "dx")
     rows, cols = dx.shape
+    _no_empty_rows(rows, cols)
     dev = dx.device
     bf16, f32 = torch.bfloat16, torch.float32
     dhptr = None if dh is None else _like(dh, (rows, cols), bf16, dev, "dh")

@@ -579,6 +579,7 @@ int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t col
                          void* y_ckpt, float* y_ckpt_sf, void* h_ckpt, float* h_ckpt_sf,
                          void* stream) {
   const bool ckpt = y_ckpt || y_ckpt_sf || h_ckpt || h_ckpt_sf;
+  if (ckpt && !fp8_fmt(ckpt_fmt)) return QCAST_ERR_FORMAT;
   int rc = check_norm(rows, cols, fmt, group, clamp_min, sf_flags, gate_kind, residual_scale,
                       weight_offset, ckpt ? ckpt_fmt : 0);
   if (rc != QCAST_OK) return rc;
@@ -646,7 +647,9 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
         (!saved_y && (w_post || gate || q || dy_out)) || !ws)
       return QCAST_ERR_NULL;
   }
-  if ((dw_post && !w_post) || (dgate && !gate)) return QCAST_ERR_NULL;
+  // these read the channel gate and w_post even where there are no rows
+  if ((dw_post && !w_post) || (dgate && !gate) || (gate_kind == QCAST_GATE_CHANNEL && !gate))
+    return QCAST_ERR_NULL;
   const int gate_align = gate_kind == QCAST_GATE_TOKEN ? 4 : 16;
   if (!aligned(dx, 16) || !aligned(dh_in, 16) || !aligned(saved_h, 16) ||
       !aligned(saved_h_sf, 4) || !aligned(saved_y, 16) || !aligned(saved_y_sf, 4) ||

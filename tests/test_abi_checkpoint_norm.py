@@ -169,6 +169,22 @@ def test_norm_backward(lib):
         assert nbwd(lib, rows=1) == ERR_DEVICE
 
 
+def test_norm_checkpoints_of_no_format(lib):
+    assert norm(lib, cf=0) == norm(lib, **{**NO_Y, "cf": 0}) == ERR_FORMAT
+    assert norm(lib, cf=0, y_ckpt=None, y_ckpt_sf=None) == ERR_FORMAT
+    if not gpu_available():       # without checkpoints the format says nothing
+        none = dict(y_ckpt=None, y_ckpt_sf=None, h_ckpt=None, h_ckpt_sf=None)
+        assert norm(lib, cf=0, **none) == norm(lib, cf=9, **none) == ERR_DEVICE
+
+
+def test_norm_backward_channel_gate_without_rows(lib):
+    # the sums over no rows are written by a kernel that reads the channel gate
+    none = dict(rows=0, dx=None, gate=None, dgate=None)
+    assert nbwd(lib, kind=1, **none) == ERR_NULL
+    if not gpu_available():
+        assert nbwd(lib, kind=2, **none) == nbwd(lib, kind=3, **none) == ERR_DEVICE
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
 

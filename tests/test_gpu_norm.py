@@ -289,3 +289,12 @@ def test_rows_of_more_than_2_31_bytes(dev):
         for x, y in list(zip(a, c)) + [(b.dh, d.dh), (b.out, d.out), (b.out_sf, d.out_sf)]:
             if x is not None:
                 assert same(x[sl].contiguous(), y)
+
+
+def test_rows_without_columns(dev):
+    e = torch.zeros(4, 0, dtype=torch.bfloat16, device=dev)
+    w = torch.zeros(0, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(pq.QcastError):
+        pq.qcast_norm_per_token(e, w)
+    with pytest.raises(pq.QcastError):
+        pq.qcast_norm_backward_per_token(e, e, torch.ones(4, device=dev), w)

@@ -15,15 +15,18 @@
 // What it must move: y and h read, h' and the codes written (7 bytes per
 // element with 8-bit codes, 9 with both 8-bit checkpoints), so it is bound by
 // HBM bandwidth, or by the launch for a few rows. 4096 x 7168 with a channel
-// gate and both checkpoints: 53 us, 5.0 TB/s (a copy of as many bytes: 42.5);
-// without checkpoints 44; one row 4.3.
+// gate and both checkpoints: 49 us, 5.4 TB/s (a copy of as many bytes: 42.5);
+// without checkpoints 40; one row 3.7.
 //
 // gfx950 design. A workgroup holds a row in registers from the load to the
 // last store (a lane kC chunks of 8 columns), so the row crosses HBM once
 // although it is reduced twice; each sum is a wave butterfly and one LDS trip.
 // It walks the rows with a stride of the grid, which leaves the columns'
-// factors in registers and lets the next row be loaded while this one is
-// worked on. The up to three casts of a chunk (x and the two checkpoints)
+// factors in registers and lets the next two rows be loaded while this one is
+// worked on. Rows are read as buffers, so no branch stands around a load, and
+// the next row is waited for ahead of this row's stores: operations complete
+// in order, so a wait after the stores is a wait for them too (one row ahead
+// with branches 53 us, two rows 50, as buffers 49). The up to three casts of a chunk (x and the two checkpoints)
 // need three scales: lane j of a quad forms the j-th and the quad exchanges
 // them, so a lane runs the scale's 30 instructions once.
 #include "qcast_device.h"
@@ -34,9 +37,9 @@ namespace qcast {
 namespace {
 
 // Waves resident on a compute unit that the grid is sized for. One workgroup
-// of 14 waves per compute unit, the next row on its way, beats two that share
-// it (4096 x 7168: 53 us against 56; without checkpoints, where two fit in
-// the registers, 44 against 46).
+// of 14 waves per compute unit with rows on their way beats two that share it
+// (measured with one row ahead, 4096 x 7168: 53 us against 56; without
+// checkpoints, where two fit in the registers, 44 against 46).
 constexpr unsigned kResidentWaves = 16;
 constexpr int64_t kComputeUnits = 256;
 constexpr int kMaxWaves = 16;
@@ -50,17 +53,23 @@ __device__ __forceinline__ float from_quad(float v) {
 struct RowChunk {
   u32x4 y, h, gate;
 };
+// The chunk at byte `at` of a row; zeros past the row's end, and where there
+// is no such row. `row` is the same in every lane.
 template <int kGate, bool kY>
-__device__ __forceinline__ RowChunk load_row_chunk(const NormForward& p, uint32_t row,
-                                                   uint32_t jc, bool valid) {
-  const int64_t at = (int64_t)row * p.chunks + jc;
-  RowChunk c;
-  c.y = c.h = c.gate = u32x4{0u, 0u, 0u, 0u};
-  if (!valid) return c;
-  if (kY) c.y = load_stream(reinterpret_cast<const u32x4*>(p.y) + at);
-  c.h = load_stream(reinterpret_cast<const u32x4*>(p.h) + at);
-  if (kGate == kGateFull) c.gate = load_stream(reinterpret_cast<const u32x4*>(p.gate) + at);
-  return c;
+__device__ __forceinline__ void load_row_chunk(RowChunk& c, const NormForward& p, uint32_t row,
+                                               uint32_t rows, uint32_t at) {
+  const uint32_t bytes = row < rows ? p.chunks * 16 : 0;
+  const uint64_t start = (uint64_t)(row < rows ? row : 0) * p.chunks * 16;
+  if (kY) c.y = buffer_load16(row_buffer(p.y, start, bytes), at);
+  c.h = buffer_load16(row_buffer(p.h, start, bytes), at);
+  if (kGate == kGateFull) c.gate = buffer_load16(row_buffer(p.gate, start, bytes), at);
+}
+// Waits for a chunk's loads here.
+template <int kGate, bool kY>
+__device__ __forceinline__ void arrive(RowChunk& c) {
+  asm volatile("" : "+v"(c.h));
+  if constexpr (kY) asm volatile("" : "+v"(c.y));
+  if constexpr (kGate == kGateFull) asm volatile("" : "+v"(c.gate));
 }
 
 // kGate: kGateFull, kGateToken, or kGateNone for both other kinds (a channel
@@ -70,64 +79,51 @@ template <int kC, int kGate, bool kY, int kCkpt>
 __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows) {
   constexpr bool kAhead = kC == 1;
   __shared__ float part[4][kMaxWaves];
-  int buf = 0;             // alternates, so that a row's words outlive its last reader
   const uint32_t chunks = p.chunks;
+  const uint32_t lane_at = threadIdx.x * 16, chunk_step = blockDim.x * 16;
   float c[kC][8], q[kC][8];
 #pragma unroll
   for (int k = 0; k < kC; ++k) {
-    const uint32_t jc = threadIdx.x + k * blockDim.x;
-    const bool valid = jc < chunks;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    unpack8(valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero, q[k]);
-    unpack8((valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero, c[k]);
+    const uint32_t at = lane_at + k * chunk_step;
+    // without w_post, or a channel gate, an empty buffer: zeros
+    const bool channel = p.gate_kind == kGateChannel;
+    const u32x4 wq = buffer_load16<0>(row_buffer(p.w_pre, 0, chunks * 16), at);
+    const u32x4 wp = buffer_load16<0>(row_buffer(p.w_post, 0, p.w_post ? chunks * 16 : 0), at);
+    const u32x4 wg = buffer_load16<0>(row_buffer(p.gate, 0, channel ? chunks * 16 : 0), at);
+    float g[8];
+    unpack8(wq, q[k]);
+    unpack8(wp, c[k]);
+    unpack8(wg, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       q[k][i] = q[k][i] + p.offset;
       c[k][i] = p.w_post ? c[k][i] + p.offset : 1.0f;
-    }
-    if (p.gate_kind == kGateChannel) {
-      float g[8];
-      unpack8(valid ? reinterpret_cast<const u32x4*>(p.gate)[jc] : zero, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[k][i] = c[k][i] * g[i];
+      if (channel) c[k][i] = c[k][i] * g[i];
     }
   }
   // lane j of a quad: the scale of x (0), of y's checkpoint (1), of h's (2)
   const int j = threadIdx.x & 3;
   const ScaleRule rule = (kCkpt && j) ? scale_rule(kCkpt, p.h_ckpt.floor)
                                       : scale_rule(p.cast.fmt, p.cast.floor);
-  RowChunk next[kC];
+  const int waves = blockDim.x >> 6;
+  RowChunk first[kC], second[kC];
+  const uint32_t step = gridDim.x;
   if (kAhead) {
-#pragma unroll
-    for (int k = 0; k < kC; ++k) {
-      const uint32_t jc = threadIdx.x + k * blockDim.x;
-      next[k] = load_row_chunk<kGate, kY>(p, blockIdx.x, jc, jc < chunks);
-    }
+    load_row_chunk<kGate, kY>(first[0], p, blockIdx.x, rows, lane_at);
+    load_row_chunk<kGate, kY>(second[0], p, blockIdx.x + step, rows, lane_at);
   }
-  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 2) {
-    RowChunk ch[kC];
+  // The row whose chunks `mine` holds; `other` holds the one after it.
+  const auto work = [&](RowChunk (&mine)[kC], RowChunk (&other)[kC], uint32_t row, int buf) __attribute__((always_inline)) {
     const float row_gate = kGate == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
-    if constexpr (kAhead) {
-#pragma unroll
-      for (int k = 0; k < kC; ++k) {
-        const uint32_t jc = threadIdx.x + k * blockDim.x;
-        ch[k] = next[k];
-        if (row + gridDim.x < rows)
-          next[k] = load_row_chunk<kGate, kY>(p, row + gridDim.x, jc, jc < chunks);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kC; ++k) {
-        const uint32_t jc = threadIdx.x + k * blockDim.x;
-        ch[k] = load_row_chunk<kGate, kY>(p, row, jc, jc < chunks);
-      }
-    }
-    float hv[kC][8], y[kC][8];
+    float hv[kC][8], y[kC][8], full[kGate == kGateFull ? kC : 1][8];
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
-      unpack8(ch[k].h, hv[k]);
-      if (kY) unpack8(ch[k].y, y[k]);
+      if (!kAhead) load_row_chunk<kGate, kY>(mine[k], p, row, rows, lane_at + k * chunk_step);
+      unpack8(mine[k].h, hv[k]);
+      if (kY) unpack8(mine[k].y, y[k]);
+      if (kGate == kGateFull) unpack8(mine[k].gate, full[k]);
     }
+    if (kAhead) load_row_chunk<kGate, kY>(mine[0], p, row + 2 * step, rows, lane_at);
     if constexpr (kY) {
       float r1 = 1.0f;
       if (p.w_post) {
@@ -136,19 +132,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
         for (int k = 0; k < kC; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(y[k][i], y[k][i], ss);
-        ss = block_sum(ss, part[buf]);
+        ss = block_sum(ss, part[buf], waves);
         r1 = inv_sqrt(__builtin_fmaf(ss, p.inv_n, p.eps));
         if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r1;
       }
       if (kGate == kGateToken) r1 = r1 * row_gate;
 #pragma unroll
       for (int k = 0; k < kC; ++k) {
-        float g[8];
-        if (kGate == kGateFull) unpack8(ch[k].gate, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float t = y[k][i] * r1 * c[k][i];
-          if (kGate == kGateFull) t = t * g[i];
+          if (kGate == kGateFull) t = t * full[k][i];
           hv[k][i] = __builtin_fmaf(p.alpha, hv[k][i], t);
         }
       }
@@ -158,9 +152,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
     for (int k = 0; k < kC; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(hv[k][i], hv[k][i], ss);
-    ss = block_sum(ss, part[buf + 1]);
+    ss = block_sum(ss, part[buf + 1], waves);
     const float r2 = inv_sqrt(__builtin_fmaf(ss, p.inv_n, p.eps));
     if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r2;
+    if (kAhead) arrive<kGate, kY>(other[0]);
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
@@ -171,12 +166,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
       if (jc >= chunks) continue;      // the lanes of a scale group leave together
       if (kY) store_stream(reinterpret_cast<u32x4*>(p.h_out) + at, pack8_bf16(hv[k]));
       if (p.x_out) store_stream(reinterpret_cast<u32x4*>(p.x_out) + at, pack8_bf16(x));
-      float amax = run_max(absmax8(x), p.cast.shift);
+      float amax = run_max(absmax8_of(x), p.cast.shift);
       if (kCkpt) {
-        const float ha = lane_group_max<16>(absmax8(hv[k]));
+        const float ha = lane_group_max<16>(absmax8_of(hv[k]));
         amax = j == 2 ? ha : amax;
         if (kY) {
-          const float ya = lane_group_max<16>(absmax8(y[k]));
+          const float ya = lane_group_max<16>(absmax8_of(y[k]));
           amax = j == 1 ? ya : amax;
         }
       }
@@ -199,6 +194,21 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
         }
       }
     }
+  };
+  uint32_t row = blockIdx.x;
+  if constexpr (kAhead) {
+    while (true) {
+      work(first, second, row, 0);
+      row = __builtin_amdgcn_readfirstlane(row + step);
+      if (row >= rows) break;
+      work(second, first, row, 2);
+      row = __builtin_amdgcn_readfirstlane(row + step);
+      if (row >= rows) break;
+    }
+  } else {
+    int buf = 0;
+    for (; row < rows; row = __builtin_amdgcn_readfirstlane(row + step), buf ^= 2)
+      work(first, first, row, buf);
   }
 }
 

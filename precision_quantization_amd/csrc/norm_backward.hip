@@ -198,6 +198,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
   if (kKeep)
     next = load_chunk<kSaved, kGate, kY>(p, blockIdx.x, threadIdx.x, threadIdx.x < chunks);
   int parity = 0;
+  const int waves = blockDim.x >> 6;
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
     Chunk ch[kC];
     if constexpr (kKeep) {
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
       if constexpr (kKeep) kept = v;
       else store_sums(acc + 4 * k * 1024, s_pre);
     }
-    block_sum3(s1, s2, s3, part[parity]);
+    block_sum3(s1, s2, s3, part[parity], waves);
     const float m1 = s1 * p.inv_n;
     const float along = s2 - r2 * m1 * s3;      // sum dH * a * c, without a token gate
     if (kY && kGate == kGateToken && p.dgate && threadIdx.x == 0)

@@ -11,6 +11,22 @@
 
 namespace qcast {
 
+// A row in memory as a buffer of `bytes` bytes (base and bytes the same in
+// every lane): a lane past its end loads zeros, without a branch around the
+// load. The compiler then knows how many operations follow one, and a wait for
+// a row that was asked for earlier is not a wait for everything.
+using RowBuffer = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ RowBuffer row_buffer(const void* base, uint64_t at, uint32_t bytes) {
+  constexpr int kRawDwords = 0x00027000;       // no swizzle, no stride, 32-bit data
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + at, 0, bytes, kRawDwords);
+}
+constexpr int kNonTemporal = 2;
+template <int kPolicy = kNonTemporal>
+__device__ __forceinline__ u32x4 buffer_load16(RowBuffer b, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, kPolicy);
+}
+
 // Sums over the wave64: every lane ends with the same bits (each step adds a
 // pair of lanes' values, and fp32 addition commutes).
 template <int kCtrl>
@@ -38,11 +54,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 // in every thread: `part` holds one row of 4 words per wave. One barrier;
 // every lane then reads one wave's row (one LDS trip, however many waves) and
 // the rows are added across the 16 lanes.
-__device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float (*part)[4]) {
+__device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float (*part)[4],
+                                           int waves) {
   a = wave_sum(a);
   b = wave_sum(b);
   c = wave_sum(c);
-  const int waves = blockDim.x >> 6;
   if (waves == 1) return;
   typedef float f32x4 __attribute__((ext_vector_type(4)));
   if ((threadIdx.x & 63) == 0)
@@ -54,6 +70,17 @@ __device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float (
   a = row16_sum(v.x);
   b = row16_sum(v.y);
   c = row16_sum(v.z);
+}
+
+// Abs-max of 8 values, as absmax8. Starting from zero, every step is one
+// v_max3_f32 with its operands' signs dropped; the first pair by itself costs
+// three instructions where the compiler cannot see that its values came from
+// arithmetic.
+__device__ __forceinline__ float absmax8_of(const float v[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
+  return m;
 }
 
 // Abs-max over the aligned run of 2^shift lanes (4, 8 or 16; shift is the
@@ -95,9 +122,8 @@ __device__ __forceinline__ void decode8(const u32x2& w, float sf, float v[8]) {
 
 // Two fp32 -> two bf16 (nearest even) in one dword (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(a));
-  const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(b));
-  return lo | (hi << 16);
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 __device__ __forceinline__ u32x4 pack8_bf16(const float v[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
@@ -180,7 +206,7 @@ __device__ __forceinline__ Scale scale_by(const ScaleRule& r, float amax) {
 // The lanes of a scale group call this together, lane = jc mod 64.
 __device__ __forceinline__ void cast_chunk(const RowCast& rc, uint32_t row, uint32_t jc,
                                            uint32_t chunks, const float v[8]) {
-  Scale s = scale_by(scale_rule(rc.fmt, rc.floor), run_max(absmax8(v), rc.shift));
+  Scale s = scale_by(scale_rule(rc.fmt, rc.floor), run_max(absmax8_of(v), rc.shift));
   if (rc.lay.flags & kSfRound) s = round_scale_pow2(s);
   encode_chunk_any(rc, (int64_t)row * chunks + jc, v, s.inv);
   store_run_scale(rc.sf, row, jc >> rc.shift, s, rc.lay, rc.shift);
@@ -196,9 +222,8 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 }
 
 // Sum over the workgroup (at most 16 waves), the same bits in every thread.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+__device__ __forceinline__ float block_sum(float v, float* part, int waves) {
   v = wave_sum(v);
-  const int waves = blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();

@@ -26,7 +26,8 @@
 // worked on. Rows are read as buffers, so no branch stands around a load, and
 // the next row is waited for ahead of this row's stores: operations complete
 // in order, so a wait after the stores is a wait for them too (one row ahead
-// with branches 53 us, two rows 50, as buffers 49). The up to three casts of a chunk (x and the two checkpoints)
+// with branches 53 us, two rows 50, as buffers 49). The up to three casts of a
+// chunk (x and the two checkpoints)
 // need three scales: lane j of a quad forms the j-th and the quad exchanges
 // them, so a lane runs the scale's 30 instructions once.
 #include "qcast_device.h"
@@ -113,7 +114,9 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
     load_row_chunk<kGate, kY>(second[0], p, blockIdx.x + step, rows, lane_at);
   }
   // The row whose chunks `mine` holds; `other` holds the one after it.
-  const auto work = [&](RowChunk (&mine)[kC], RowChunk (&other)[kC], uint32_t row, int buf) __attribute__((always_inline)) {
+  // buf alternates, so that a row's words in `part` outlive their last reader.
+  const auto work = [&](RowChunk(&mine)[kC], RowChunk(&other)[kC], uint32_t row,
+                        int buf) __attribute__((always_inline)) {
     const float row_gate = kGate == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.0f;
     float hv[kC][8], y[kC][8], full[kGate == kGateFull ? kC : 1][8];
 #pragma unroll

@@ -72,8 +72,8 @@ __device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float (
   c = row16_sum(v.z);
 }
 
-// Abs-max of 8 values, as absmax8. Starting from zero, every step is one
-// v_max3_f32 with its operands' signs dropped; the first pair by itself costs
+// Abs-maxima of 8 and of 4 values. Starting from zero, every step is one
+// v_max3_f32 with its operands' signs dropped; a first pair by itself costs
 // three instructions where the compiler cannot see that its values came from
 // arithmetic.
 __device__ __forceinline__ float absmax8_of(const float v[8]) {
@@ -81,6 +81,10 @@ __device__ __forceinline__ float absmax8_of(const float v[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
   return m;
+}
+
+__device__ __forceinline__ float absmax4(float a, float b, float c, float d) {
+  return fmaxf(fmaxf(fmaxf(fmaxf(0.0f, fabsf(a)), fabsf(b)), fabsf(c)), fabsf(d));
 }
 
 // Abs-max over the aligned run of 2^shift lanes (4, 8 or 16; shift is the

@@ -77,8 +77,7 @@ __global__ __launch_bounds__(kThreads) void recast_kernel(RecastTile p, TileWalk
     for (int i = 0; i < 4; ++i) decode_word<kIn>(raw[i][w], sf[i], t[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      m[4 * w + j] = __float_as_uint(fmaxf(fmaxf(fabsf(t[0][j]), fabsf(t[1][j])),
-                                           fmaxf(fabsf(t[2][j]), fabsf(t[3][j]))));
+      m[4 * w + j] = __float_as_uint(absmax4(t[0][j], t[1][j], t[2][j], t[3][j]));
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {        // bit 4: upper 8 channels

@@ -50,8 +50,7 @@ __device__ __forceinline__ void column_max(const float (&v)[4][8], float* out) {
   uint32_t m[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    m[j] = __float_as_uint(fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])),
-                                 fmaxf(fabsf(v[2][j]), fabsf(v[3][j]))));
+    m[j] = __float_as_uint(absmax4(v[0][j], v[1][j], v[2][j], v[3][j]));
   uint32_t n[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -230,8 +229,8 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
     uint32_t m[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      m[i] = __float_as_uint(absmax8(dg[i]));
-      m[4 + i] = __float_as_uint(absmax8(du[i]));
+      m[i] = __float_as_uint(absmax8_of(dg[i]));
+      m[4 + i] = __float_as_uint(absmax8_of(du[i]));
     }
     Scale s = group_scale<kFmt>(row_max8(m), p.floor);
     if (kLayout && (p.lay.flags & kSfRound)) s = round_scale_pow2(s);

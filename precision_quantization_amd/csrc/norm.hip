@@ -43,6 +43,12 @@ namespace {
 // checkpoints, where two fit in the registers, 44 against 46).
 constexpr unsigned kResidentWaves = 16;
 constexpr int64_t kComputeUnits = 256;
+// Inputs of up to this many bytes are all read with plain loads: what of them
+// the 256 MB Infinity Cache still holds comes from there. Of larger ones, which
+// would push each other out, only y is, which the block has just written
+// (8192 x 2048, 67 MB: 26 us against 29, 16384 x 512, 34 MB: 14 against 17;
+// 4096 x 7168, 117 MB, inputs long unused: 50 against 49).
+constexpr int64_t kCachedBytes = int64_t(96) << 20;
 constexpr int kMaxWaves = 16;
 
 // The value lane j of the quad holds.
@@ -56,14 +62,15 @@ struct RowChunk {
 };
 // The chunk at byte `at` of a row; zeros past the row's end, and where there
 // is no such row. `row` is the same in every lane.
-template <int kGate, bool kY>
+template <int kGate, bool kY, bool kCached>
 __device__ __forceinline__ void load_row_chunk(RowChunk& c, const NormForward& p, uint32_t row,
                                                uint32_t rows, uint32_t at) {
   const uint32_t bytes = row < rows ? p.chunks * 16 : 0;
   const uint64_t start = (uint64_t)(row < rows ? row : 0) * p.chunks * 16;
-  if (kY) c.y = buffer_load16(row_buffer(p.y, start, bytes), at);
-  c.h = buffer_load16(row_buffer(p.h, start, bytes), at);
-  if (kGate == kGateFull) c.gate = buffer_load16(row_buffer(p.gate, start, bytes), at);
+  constexpr int kPolicy = kCached ? 0 : kNonTemporal;
+  if (kY) c.y = buffer_load16<0>(row_buffer(p.y, start, bytes), at);
+  c.h = buffer_load16<kPolicy>(row_buffer(p.h, start, bytes), at);
+  if (kGate == kGateFull) c.gate = buffer_load16<kPolicy>(row_buffer(p.gate, start, bytes), at);
 }
 // Waits for a chunk's loads here.
 template <int kGate, bool kY>
@@ -76,7 +83,7 @@ __device__ __forceinline__ void arrive(RowChunk& c) {
 // kGate: kGateFull, kGateToken, or kGateNone for both other kinds (a channel
 // gate is one of the column factors). kY: there is a block output. kCkpt: the
 // checkpoints' format, 0 for none.
-template <int kC, int kGate, bool kY, int kCkpt>
+template <int kC, int kGate, bool kY, int kCkpt, bool kCached>
 __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows) {
   constexpr bool kAhead = kC == 1;
   __shared__ float part[4][kMaxWaves];
@@ -110,8 +117,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
   RowChunk first[kC], second[kC];
   const uint32_t step = gridDim.x;
   if (kAhead) {
-    load_row_chunk<kGate, kY>(first[0], p, blockIdx.x, rows, lane_at);
-    load_row_chunk<kGate, kY>(second[0], p, blockIdx.x + step, rows, lane_at);
+    load_row_chunk<kGate, kY, kCached>(first[0], p, blockIdx.x, rows, lane_at);
+    load_row_chunk<kGate, kY, kCached>(second[0], p, blockIdx.x + step, rows, lane_at);
   }
   // The row whose chunks `mine` holds; `other` holds the one after it.
   // buf alternates, so that a row's words in `part` outlive their last reader.
@@ -121,12 +128,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
     float hv[kC][8], y[kC][8], full[kGate == kGateFull ? kC : 1][8];
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
-      if (!kAhead) load_row_chunk<kGate, kY>(mine[k], p, row, rows, lane_at + k * chunk_step);
+      if (!kAhead) load_row_chunk<kGate, kY, kCached>(mine[k], p, row, rows, lane_at + k * chunk_step);
       unpack8(mine[k].h, hv[k]);
       if (kY) unpack8(mine[k].y, y[k]);
       if (kGate == kGateFull) unpack8(mine[k].gate, full[k]);
     }
-    if (kAhead) load_row_chunk<kGate, kY>(mine[0], p, row + 2 * step, rows, lane_at);
+    if (kAhead) load_row_chunk<kGate, kY, kCached>(mine[0], p, row + 2 * step, rows, lane_at);
     if constexpr (kY) {
       float r1 = 1.0f;
       if (p.w_post) {
@@ -215,19 +222,19 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
   }
 }
 
-template <int kC, int kGate, bool kY>
+template <int kC, bool kCached, int kGate, bool kY>
 auto pick_ckpt(const NormForward& p) {
   const int f = (p.h_ckpt.q || p.y_ckpt.q) ? p.h_ckpt.fmt : 0;
-  return f == 0       ? norm_kernel<kC, kGate, kY, 0>
-         : f == kE4M3 ? norm_kernel<kC, kGate, kY, kE4M3>
-                      : norm_kernel<kC, kGate, kY, kE5M2>;
+  return f == 0       ? norm_kernel<kC, kGate, kY, 0, kCached>
+         : f == kE4M3 ? norm_kernel<kC, kGate, kY, kE4M3, kCached>
+                      : norm_kernel<kC, kGate, kY, kE5M2, kCached>;
 }
-template <int kC>
+template <int kC, bool kCached>
 auto pick(const NormForward& p) {
-  return !p.y                        ? pick_ckpt<kC, kGateNone, false>(p)
-         : p.gate_kind == kGateFull  ? pick_ckpt<kC, kGateFull, true>(p)
-         : p.gate_kind == kGateToken ? pick_ckpt<kC, kGateToken, true>(p)
-                                     : pick_ckpt<kC, kGateNone, true>(p);
+  return !p.y                        ? pick_ckpt<kC, kCached, kGateNone, false>(p)
+         : p.gate_kind == kGateFull  ? pick_ckpt<kC, kCached, kGateFull, true>(p)
+         : p.gate_kind == kGateToken ? pick_ckpt<kC, kCached, kGateToken, true>(p)
+                                     : pick_ckpt<kC, kCached, kGateNone, true>(p);
 }
 
 }  // namespace
@@ -235,12 +242,15 @@ auto pick(const NormForward& p) {
 hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream) {
   if (rows == 0 || p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
+  const int inputs = 1 + (p.y != nullptr) + (p.gate_kind == kGateFull);
+  const bool cached = rows * p.chunks * 16 * inputs <= kCachedBytes;
   const int kc = p.chunks > 1024 ? 2 : 1;
   const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
   const unsigned waves = threads / 64;
   const int64_t resident = kComputeUnits * (waves < kResidentWaves ? kResidentWaves / waves : 1);
   const unsigned grid = (unsigned)(rows < resident ? rows : resident);
-  auto kernel = kc == 1 ? pick<1>(p) : pick<2>(p);
+  auto kernel = kc == 1 ? (cached ? pick<1, true>(p) : pick<1, false>(p))
+                        : (cached ? pick<2, true>(p) : pick<2, false>(p));
   launch_kernel(kernel, dim3(grid), dim3(threads), 0, stream, p, (uint32_t)rows);
   return hipGetLastError();
 }

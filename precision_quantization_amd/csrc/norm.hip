@@ -128,7 +128,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
     float hv[kC][8], y[kC][8], full[kGate == kGateFull ? kC : 1][8];
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
-      if (!kAhead) load_row_chunk<kGate, kY, kCached>(mine[k], p, row, rows, lane_at + k * chunk_step);
+      if (!kAhead)
+        load_row_chunk<kGate, kY, kCached>(mine[k], p, row, rows, lane_at + k * chunk_step);
       unpack8(mine[k].h, hv[k]);
       if (kY) unpack8(mine[k].y, y[k]);
       if (kGate == kGateFull) unpack8(mine[k].gate, full[k]);

@@ -16,8 +16,9 @@
 // to 8 bits have derivative one.
 //
 // One reduction round per row: da depends on mean(g * xh), but linearly, so
-// with b = dh' + r2 * g the sums S1 = sum g * xh, S2 = sum b * c and
-// S3 = sum xh * c, c = gate * wp * a, are taken together and
+// with b = dh' + r2 * g (then dH = b - r2 * mean(g * xh) * xh) the sums
+// S1 = sum g * xh, S2 = sum b * c and S3 = sum xh * c, c = gate * wp * a, are
+// taken together and
 //   sum da * a = S2 - r2 * (S1 / n) * S3.
 //
 // gfx950 design. Workgroups walk the rows with a stride, so a lane meets the
@@ -35,7 +36,7 @@
 // What it must move: dx, dh', both saved tensors, dh and the codes of dy (9
 // bytes per element from 8-bit checkpoints, 11 from bf16), plus 8 bytes per
 // column and workgroup of partial sums. 4096 x 7168, channel gate, from
-// checkpoints: 55 us, of which the join takes 5 (a copy of 264 MB: 42).
+// checkpoints: 54 us, of which the join takes 5 (a copy of 264 MB: 42).
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -125,35 +126,38 @@ __device__ __forceinline__ void saved_values(const u32x4& raw, float sf, float v
 
 // The factors of a chunk's columns: q = w_pre + offset, and c = wp (times a
 // channel gate; 1 without w_post).
-__device__ __forceinline__ void column_factors(const NormBackward& p, uint32_t jc, bool valid,
-                                               float q[8], float c[8]) {
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  unpack8(valid ? reinterpret_cast<const u32x4*>(p.w_pre)[jc] : zero, q);
-  unpack8((valid && p.w_post) ? reinterpret_cast<const u32x4*>(p.w_post)[jc] : zero, c);
+__device__ __forceinline__ void column_factors(const NormBackward& p, uint32_t jc, float q[8],
+                                               float c[8]) {
+  // past the row, without w_post or a channel gate: zeros of an empty buffer
+  const bool channel = p.gate_kind == kGateChannel;
+  const uint32_t n = p.chunks * 16;
+  const u32x4 wq = buffer_load16<0>(row_buffer(p.w_pre, 0, n), jc * 16);
+  const u32x4 wp = buffer_load16<0>(row_buffer(p.w_post, 0, p.w_post ? n : 0), jc * 16);
+  const u32x4 wg = buffer_load16<0>(row_buffer(p.gate, 0, channel ? n : 0), jc * 16);
+  float g[8];
+  unpack8(wq, q);
+  unpack8(wp, c);
+  unpack8(wg, g);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     q[i] = q[i] + p.offset;
     c[i] = p.w_post ? c[i] + p.offset : 1.0f;
-  }
-  if (p.gate_kind == kGateChannel) {
-    float g[8];
-    unpack8(valid ? reinterpret_cast<const u32x4*>(p.gate)[jc] : zero, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = c[i] * g[i];
+    if (channel) c[i] = c[i] * g[i];
   }
 }
 
 // The fp32 values of a chunk that both halves of a row's work use.
 struct Values {
-  float x[8], a[8], gx[8], dh[8], c[8];   // xh, a, dx * q, dh', gate * wp
+  float x[8], a[8], b[8], c[8];      // xh, a, dh' + r2 * dx * q, gate * wp
 };
 
 template <int kSaved, int kGate, bool kY>
 __device__ __forceinline__ Values chunk_values(const Chunk& ch, const float q[8],
-                                               const float c[8], float dx[8]) {
+                                               const float c[8], float dx[8],
+                                               float gx[8]) {
   Values v;
   unpack8(ch.dx, dx);
-  unpack8(ch.dh, v.dh);
+  unpack8(ch.dh, v.b);
   // code * sf * r in one product: code * (sf * r)
   saved_values<kSaved>(ch.hs, kSaved ? ch.hsf * ch.r2 : ch.r2, v.x);
   if (kY) saved_values<kSaved>(ch.ys, kSaved ? ch.ysf * ch.r1 : ch.r1, v.a);
@@ -161,7 +165,8 @@ __device__ __forceinline__ Values chunk_values(const Chunk& ch, const float q[8]
   if (kGate == kGateFull) unpack8(ch.gate, g);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v.gx[i] = dx[i] * q[i];
+    gx[i] = dx[i] * q[i];
+    v.b[i] = __builtin_fmaf(ch.r2, gx[i], v.b[i]);
     v.c[i] = kGate == kGateFull ? c[i] * g[i] : c[i];
   }
   return v;
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
 #pragma unroll
   for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = 0.0f;
   if constexpr (kKeep) {
-    column_factors(p, threadIdx.x, threadIdx.x < chunks, q[0], c[0]);
+    column_factors(p, threadIdx.x, q[0], c[0]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4 * kC; ++i) acc[i * 1024 + threadIdx.x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -223,17 +228,17 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
-      if (!kKeep) column_factors(p, jc, jc < chunks, q[k], c[k]);
-      float dx[8];
-      const Values v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx);
+      if (!kKeep) column_factors(p, jc, q[k], c[k]);
+      float dx[8], gx[8];
+      const Values v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx, gx);
       if constexpr (!kKeep) load_sums(acc + 4 * k * 1024, s_pre);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s1 = __builtin_fmaf(v.gx[i], v.x[i], s1);
+        s1 = __builtin_fmaf(gx[i], v.x[i], s1);
         s_pre[i] = __builtin_fmaf(dx[i], v.x[i], s_pre[i]);
         if (kY) {
           const float cc = v.a[i] * v.c[i];
-          s2 = __builtin_fmaf(__builtin_fmaf(r2, v.gx[i], v.dh[i]), cc, s2);
+          s2 = __builtin_fmaf(v.b[i], cc, s2);
           s3 = __builtin_fmaf(v.x[i], cc, s3);
         }
       }
@@ -242,7 +247,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
     }
     block_sum3(s1, s2, s3, part[parity], waves);
     const float m1 = s1 * p.inv_n;
-    const float along = s2 - r2 * m1 * s3;      // sum dH * a * c, without a token gate
+    const float r2m1 = r2 * m1;
+    const float along = s2 - r2m1 * s3;      // sum dH * a * c, without a token gate
     if (kY && kGate == kGateToken && p.dgate && threadIdx.x == 0)
       static_cast<float*>(p.dgate)[row] = along;
     const float m2 = (kY && p.w_post) ? along * row_gate * p.inv_n : 0.0f;
@@ -253,21 +259,22 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
       if constexpr (kKeep) {
         v = kept;
       } else {
-        float dx[8];
-        column_factors(p, jc, jc < chunks, q[k], c[k]);
-        v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx);
+        float dx[8], gx[8];
+        column_factors(p, jc, q[k], c[k]);
+        v = chunk_values<kSaved, kGate, kY>(ch[k], q[k], c[k], dx, gx);
       }
       float g[8], d[8], out[8];
       if (kFull) unpack8(ch[k].gate, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = __builtin_fmaf(r2, __builtin_fmaf(-v.x[i], m1, v.gx[i]), v.dh[i]);
+        d[i] = __builtin_fmaf(-v.x[i], r2m1, v.b[i]);
         out[i] = p.alpha * d[i];
       }
       const int64_t at = (int64_t)row * chunks + jc;
       const u32x4 dh_bits = pack8_bf16(out);
-      // 4096 x 7168: 57 us against 62, 8192 x 5120: 77 against 89 (with an
-      // elementwise gate it spills registers: 1000 x 2048 15.7 against 14.1)
+      // 4096 x 7168: 54 us against 57, 8192 x 5120 in bf16: 82 against 99 (with
+      // an elementwise gate there are no registers for it: 1000 x 2048 15.4
+      // against 14.3)
       if constexpr (kKeep && !kFull) arrive<kSaved, kGate, kY>(next);
       if (jc < chunks) store_stream(reinterpret_cast<u32x4*>(p.dh_out) + at, dh_bits);
       if (kY) {
@@ -306,7 +313,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackward p, uin
       float* o = p.ws + (int64_t)blockIdx.x * 2 * 8 * chunks + 8 * jc;
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<f32x4*>(o + i) = f32x4{s_pre[i], s_pre[i + 1], s_pre[i + 2], s_pre[i + 3]};
+        *reinterpret_cast<f32x4*>(o + i) =
+            f32x4{s_pre[i], s_pre[i + 1], s_pre[i + 2], s_pre[i + 3]};
         if (kY)
           *reinterpret_cast<f32x4*>(o + 8 * chunks + i) =
               f32x4{s_post[i], s_post[i + 1], s_post[i + 2], s_post[i + 3]};

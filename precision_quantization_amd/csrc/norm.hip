@@ -15,8 +15,9 @@
 // What it must move: y and h read, h' and the codes written (7 bytes per
 // element with 8-bit codes, 9 with both 8-bit checkpoints), so it is bound by
 // HBM bandwidth, or by the launch for a few rows. 4096 x 7168 with a channel
-// gate and both checkpoints: 49 us, 5.4 TB/s (a copy of as many bytes: 42.5);
-// without checkpoints 40; one row 3.7.
+// gate and both checkpoints: 48 us, 5.5 TB/s (a copy of as many bytes: 42.5;
+// with the barriers, the loads or the stores taken out 46, 44 or 47: its vector
+// instructions are the most of it); without checkpoints 37; one row 3.6.
 //
 // gfx950 design. A workgroup holds a row in registers from the load to the
 // last store (a lane kC chunks of 8 columns), so the row crosses HBM once
@@ -30,6 +31,8 @@
 // chunk (x and the two checkpoints)
 // need three scales: lane j of a quad forms the j-th and the quad exchanges
 // them, so a lane runs the scale's 30 instructions once.
+#include <type_traits>
+
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -148,13 +151,22 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
         if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r1;
       }
       if (kGate == kGateToken) r1 = r1 * row_gate;
+      if (kAhead && p.alpha != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hv[0][i] = p.alpha * hv[0][i];
+      }
 #pragma unroll
       for (int k = 0; k < kC; ++k) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float t = y[k][i] * r1 * c[k][i];
-          if (kGate == kGateFull) t = t * full[k][i];
-          hv[k][i] = __builtin_fmaf(p.alpha, hv[k][i], t);
+          const float a = y[k][i] * r1;
+          if constexpr (kAhead) {
+            hv[k][i] = kGate == kGateFull ? __builtin_fmaf(a * c[k][i], full[k][i], hv[k][i])
+                                          : __builtin_fmaf(a, c[k][i], hv[k][i]);
+          } else {
+            const float t = kGate == kGateFull ? a * c[k][i] * full[k][i] : a * c[k][i];
+            hv[k][i] = __builtin_fmaf(p.alpha, hv[k][i], t);
+          }
         }
       }
     }
@@ -170,13 +182,19 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
 #pragma unroll
     for (int k = 0; k < kC; ++k) {
       const uint32_t jc = threadIdx.x + k * blockDim.x;
-      const int64_t at = (int64_t)row * chunks + jc;
+      // The chunk: the row's first one in a scalar base and an index into the
+      // row, or (two chunks a lane, where these offsets would take registers
+      // for the whole loop) one index.
+      const uint64_t first_chunk = (uint64_t)row * chunks;
+      const uint64_t at = kAhead ? first_chunk : 0;
+      using Index = std::conditional_t<kAhead, uint32_t, uint64_t>;
+      const Index ix = kAhead ? jc : (Index)(first_chunk + jc);
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = hv[k][i] * r2 * q[k][i];
       if (jc >= chunks) continue;      // the lanes of a scale group leave together
-      if (kY) store_stream(reinterpret_cast<u32x4*>(p.h_out) + at, pack8_bf16(hv[k]));
-      if (p.x_out) store_stream(reinterpret_cast<u32x4*>(p.x_out) + at, pack8_bf16(x));
+      if (kY) store_stream(reinterpret_cast<u32x4*>(p.h_out) + at + ix, pack8_bf16(hv[k]));
+      if (p.x_out) store_stream(reinterpret_cast<u32x4*>(p.x_out) + at + ix, pack8_bf16(x));
       float amax = run_max(absmax8_of(x), p.cast.shift);
       if (kCkpt) {
         const float ha = lane_group_max<16>(absmax8_of(hv[k]));
@@ -189,18 +207,18 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormForward p, uint32_t rows
       Scale s = scale_by(rule, amax);
       if ((p.cast.lay.flags & kSfRound) && !(kCkpt && j)) s = round_scale_pow2(s);
       if (p.cast.q) {
-        encode_chunk_any(p.cast, at, x, kCkpt ? from_quad<0>(s.inv) : s.inv);
+        encode_chunk_any(p.cast, at, ix, x, kCkpt ? from_quad<0>(s.inv) : s.inv);
         store_run_scale(p.cast.sf, row, jc >> p.cast.shift, s, p.cast.lay, p.cast.shift);
       }
       if constexpr (kCkpt != 0) {
-        const int64_t sat = (int64_t)row * (chunks / 16) + jc / 16;
+        const uint64_t sat = (uint64_t)row * (chunks / 16) + jc / 16;
         const int l = threadIdx.x & 15;
         if (p.h_ckpt.q) {
-          encode_chunk<kCkpt>(p.h_ckpt, at, hv[k], from_quad<2>(s.inv));
+          encode_chunk<kCkpt>(p.h_ckpt, at, ix, hv[k], from_quad<2>(s.inv));
           if (l == 2) static_cast<float*>(p.h_ckpt.sf)[sat] = s.sf;
         }
         if (kY && p.y_ckpt.q) {
-          encode_chunk<kCkpt>(p.y_ckpt, at, y[k], from_quad<1>(s.inv));
+          encode_chunk<kCkpt>(p.y_ckpt, at, ix, y[k], from_quad<1>(s.inv));
           if (l == 1) static_cast<float*>(p.y_ckpt.sf)[sat] = s.sf;
         }
       }

@@ -151,26 +151,30 @@ __device__ __forceinline__ void store_run_scale(void* sf, uint32_t r, uint32_t k
       static_cast<uint32_t*>(sf)[idx] = w;
     }
   } else if ((lane & ((1 << shift) - 1)) == 0) {
-    static_cast<float*>(sf)[col ? kr * lay.rows_pad + r : r * lay.gpr + kr] = s.sf;
+    float* to = static_cast<float*>(sf) + (col ? r : (uint64_t)r * lay.gpr);
+    to[col ? kr * lay.rows_pad : kr] = s.sf;
   }
 }
 
-template <int kFmt>
-__device__ __forceinline__ void encode_chunk(const RowCast& rc, int64_t chunk, const float v[8],
-                                             float inv) {
+// Codes of chunk first + jc; `first`, the same in every lane, goes into a
+// scalar base.
+template <int kFmt, typename I>
+__device__ __forceinline__ void encode_chunk(const RowCast& rc, uint64_t first, I jc,
+                                             const float v[8], float inv) {
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
-  store_chunk8<kFmt>(rc.q, chunk, y);
+  store_chunk8<kFmt>(rc.q + first * code_bytes<kFmt>(8), jc, y);
 }
 // Codes of a chunk in the cast's format, with the inverse scale known.
-__device__ __forceinline__ void encode_chunk_any(const RowCast& rc, int64_t chunk,
+template <typename I>
+__device__ __forceinline__ void encode_chunk_any(const RowCast& rc, uint64_t first, I jc,
                                                  const float v[8], float inv) {
   switch (rc.fmt) {
-    case kE4M3: encode_chunk<kE4M3>(rc, chunk, v, inv); break;
-    case kE5M2: encode_chunk<kE5M2>(rc, chunk, v, inv); break;
-    case kE2M1: encode_chunk<kE2M1>(rc, chunk, v, inv); break;
-    default: encode_chunk<kE5M6>(rc, chunk, v, inv); break;
+    case kE4M3: encode_chunk<kE4M3>(rc, first, jc, v, inv); break;
+    case kE5M2: encode_chunk<kE5M2>(rc, first, jc, v, inv); break;
+    case kE2M1: encode_chunk<kE2M1>(rc, first, jc, v, inv); break;
+    default: encode_chunk<kE5M6>(rc, first, jc, v, inv); break;
   }
 }
 
@@ -212,7 +216,7 @@ __device__ __forceinline__ void cast_chunk(const RowCast& rc, uint32_t row, uint
                                            uint32_t chunks, const float v[8]) {
   Scale s = scale_by(scale_rule(rc.fmt, rc.floor), run_max(absmax8_of(v), rc.shift));
   if (rc.lay.flags & kSfRound) s = round_scale_pow2(s);
-  encode_chunk_any(rc, (int64_t)row * chunks + jc, v, s.inv);
+  encode_chunk_any(rc, 0, (int64_t)row * chunks + jc, v, s.inv);
   store_run_scale(rc.sf, row, jc >> rc.shift, s, rc.lay, rc.shift);
 }
 

@@ -545,6 +545,22 @@ NormOut = namedtuple("NormOut", "h out out_sf x rstd_post rstd_pre y_ckpt y_ckpt
                                 "h_ckpt_sf")
 NormGrad = namedtuple("NormGrad", "dh out out_sf dy dw_post dw_pre dgate")
 _HERE = nullcontext()
+try:
+    # what torch's generated code allocates with: 0.7 us a tensor, torch.empty 1.3;
+    # a small call's time is mostly its 4 to 9 outputs
+    _strided = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    def _strided(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _new(shape, dtype):
+    """A contiguous tensor on the current device."""
+    return _strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+
+
+def _new_out(t, shape, dtype, device, name):
+    return _new(shape, dtype) if t is None else _out(t, shape, dtype, device, name)
 
 
 def _placed(device, stream):
@@ -604,11 +620,11 @@ def qcast_swiglu_checkpoint(h, row_weight=None, fmt="e4m3", group=128, clamp_min
     g = group if group > 0 else 1
     sh, ctx = _placed(dev, stream)
     with ctx:
-        out = _out(out, code_shape(f, rows, cols), _code_dtype(f), dev, "out")
+        out = _new_out(out, code_shape(f, rows, cols), _code_dtype(f), dev, "out")
         shape, dt = sf_layout_shape(rows, cols, g, sf_flags)
-        out_sf = _out(out_sf, shape, dt, dev, "out_sf")
-        ckpt = _out(ckpt, (rows, 2 * cols), _code_dtype(cf), dev, "ckpt")
-        ckpt_sf = _out(ckpt_sf, (rows, 2 * cols // g), torch.float32, dev, "ckpt_sf")
+        out_sf = _new_out(out_sf, shape, dt, dev, "out_sf")
+        ckpt = _new_out(ckpt, (rows, 2 * cols), _code_dtype(cf), dev, "ckpt")
+        ckpt_sf = _new_out(ckpt_sf, (rows, 2 * cols // g), torch.float32, dev, "ckpt_sf")
         check(load().qcast_swiglu_checkpoint(
             h.data_ptr(), rows, cols, wptr, f, group, clamp_min, sf_flags, swiglu_clamp,
             out.data_ptr(), out_sf.data_ptr(), cf, ckpt.data_ptr(), ckpt_sf.data_ptr(), sh),
@@ -642,21 +658,19 @@ def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4
     sh, ctx = _placed(dev, stream)
     with ctx:
         dt8 = _code_dtype(f)
-        dh = torch.empty(rows, two_n, dtype=dt8, device=dev)
+        dh = _new((rows, two_n), dt8)
         shape, dt = sf_layout_shape(rows, two_n, 128, sf_flags)
-        dh_sf = torch.empty(*shape, dtype=dt, device=dev)
+        dh_sf = _new(shape, dt)
         dh_t = dh_t_sf = v_t = v_t_sf = dw = ws = None
         if transposed:
-            dh_t = torch.empty(two_n, rows_t, dtype=dt8, device=dev)
-            v_t = torch.empty(cols, rows_t, dtype=dt8, device=dev)
-            dh_t_sf = torch.empty(*sf_layout_shape(two_n, rows_t, 128, sf_flags)[0], dtype=dt,
-                                  device=dev)
-            v_t_sf = torch.empty(*sf_layout_shape(cols, rows_t, 128, sf_flags)[0], dtype=dt,
-                                 device=dev)
+            dh_t = _new((two_n, rows_t), dt8)
+            v_t = _new((cols, rows_t), dt8)
+            dh_t_sf = _new(sf_layout_shape(two_n, rows_t, 128, sf_flags)[0], dt)
+            v_t_sf = _new(sf_layout_shape(cols, rows_t, 128, sf_flags)[0], dt)
         if weight_grad:
-            dw = torch.empty(rows, dtype=torch.float32, device=dev)
+            dw = _new((rows,), torch.float32)
             if cols > 128:
-                ws = torch.empty(rows * (cols // 128), dtype=torch.float32, device=dev)
+                ws = _new((rows * (cols // 128),), torch.float32)
         check(load().qcast_swiglu_backward_checkpoint(
             ckpt.data_ptr(), sfptr, dvptr, rows, cols, wptr, cf, f, group, clamp_min, sf_flags,
             swiglu_clamp, dh.data_ptr(), dh_sf.data_ptr(), _ptr(dh_t), _ptr(dh_t_sf), _ptr(v_t),
@@ -685,9 +699,9 @@ def qcast_recast_per_channel_T(q, sf, fmt="e4m3", group=128, clamp_min=0.0, sf_f
     rows_t = (rows + 127) // 128 * 128
     sh, ctx = _placed(dev, stream)
     with ctx:
-        out = _out(out, (cols, rows_t), _code_dtype(f), dev, "out")
+        out = _new_out(out, (cols, rows_t), _code_dtype(f), dev, "out")
         shape, dt = sf_layout_shape(cols, rows_t, 128, sf_flags)
-        out_sf = _out(out_sf, shape, dt, dev, "out_sf")
+        out_sf = _new_out(out_sf, shape, dt, dev, "out_sf")
         check(load().qcast_recast_per_channel_T(
             q.data_ptr(), sfptr, rows, cols, cf, in_group, f, group, clamp_min, sf_flags,
             out.data_ptr(), out_sf.data_ptr(), sh), "qcast_recast_per_channel_T")
@@ -740,22 +754,22 @@ def qcast_norm_per_token(h, w_pre, y=None, w_post=None, gate=None, residual_scal
         raise QcastError(4, "ckpt_fmt must be an 8-bit format (e4m3 or e5m2)")
     sh, ctx = _placed(dev, stream)
     with ctx:
-        h_out = h if y is None else torch.empty(rows, cols, dtype=bf16, device=dev)
+        h_out = h if y is None else _new((rows, cols), bf16)
         out = out_sf = x = r1 = yc = yc_sf = hc = hc_sf = None
         if want_codes:
-            out = torch.empty(*code_shape(f, rows, cols), dtype=_code_dtype(f), device=dev)
+            out = _new(code_shape(f, rows, cols), _code_dtype(f))
             shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
-            out_sf = torch.empty(*shape, dtype=dt, device=dev)
+            out_sf = _new(shape, dt)
         if want_x:
-            x = torch.empty(rows, cols, dtype=bf16, device=dev)
-        r2 = torch.empty(rows, dtype=f32, device=dev)
+            x = _new((rows, cols), bf16)
+        r2 = _new((rows,), f32)
         if w_post is not None:
-            r1 = torch.empty(rows, dtype=f32, device=dev)
+            r1 = _new((rows,), f32)
         if cf:
-            hc = torch.empty(rows, cols, dtype=_code_dtype(cf), device=dev)
-            hc_sf = torch.empty(rows, cols // 128, dtype=f32, device=dev)
+            hc = _new((rows, cols), _code_dtype(cf))
+            hc_sf = _new((rows, cols // 128), f32)
             if y is not None:
-                yc, yc_sf = torch.empty_like(hc), torch.empty_like(hc_sf)
+                yc, yc_sf = _new((rows, cols), _code_dtype(cf)), _new((rows, cols // 128), f32)
         check(load().qcast_norm_per_token(
             yptr, h.data_ptr(), rows, cols, wpptr, wqptr, gptr, kind, residual_scale,
             weight_offset, eps, f, group, clamp_min, sf_flags,
@@ -820,22 +834,22 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
     kind, gptr = _gate_arg(gate, rows, cols, dev)
     stream_handle, ctx = _placed(dev, stream)
     with ctx:
-        dh_out = torch.empty(rows, cols, dtype=bf16, device=dev)
+        dh_out = _new((rows, cols), bf16)
         out = out_sf = dy = dw_post = dgate = ws = None
         if saved_y is not None:
             if want_codes:
-                out = torch.empty(*code_shape(f, rows, cols), dtype=_code_dtype(f), device=dev)
+                out = _new(code_shape(f, rows, cols), _code_dtype(f))
                 shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
-                out_sf = torch.empty(*shape, dtype=dt, device=dev)
+                out_sf = _new(shape, dt)
             if want_dy:
-                dy = torch.empty(rows, cols, dtype=bf16, device=dev)
-        dw_pre = torch.empty(cols, dtype=f32, device=dev)
+                dy = _new((rows, cols), bf16)
+        dw_pre = _new((cols,), f32)
         if w_post is not None:
-            dw_post = torch.empty(cols, dtype=f32, device=dev)
+            dw_post = _new((cols,), f32)
         if kind:
-            dgate = torch.empty(*gate.shape, dtype=bf16 if kind == GATE_FULL else f32, device=dev)
+            dgate = _new(tuple(gate.shape), bf16 if kind == GATE_FULL else f32)
         if rows:
-            ws = torch.empty(norm_ws_rows(rows, cols) * 2 * cols, dtype=f32, device=dev)
+            ws = _new((norm_ws_rows(rows, cols) * 2 * cols,), f32)
         check(load().qcast_norm_backward_per_token(
             dx.data_ptr(), dhptr, rows, cols, sf, shptr, shsf, syptr, sysf, r1ptr, r2ptr, wpptr,
             wqptr, gptr, kind, residual_scale, weight_offset, f, group, clamp_min, sf_flags,

@@ -567,7 +567,7 @@ def _placed(device, stream):
     """The handle of the stream a call runs on and the context in which it
     allocates: outputs and workspaces come from that stream's pool, so memory
     still in use on the current stream is never handed to another one."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if device.index == here:
         current = torch._C._cuda_getCurrentRawStream(here)     # 2 us less than a Stream object
     else:
@@ -599,10 +599,10 @@ def _codes(q, name):
 
 def _like(t, shape, dtype, device, name):
     """An input that has to have this shape and type; returns its pointer."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
-            t.device != device or not t.is_contiguous():
-        raise QcastError(2, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and \
+            t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise QcastError(2, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
 
 
 def qcast_swiglu_checkpoint(h, row_weight=None, fmt="e4m3", group=128, clamp_min=0.0, sf_flags=0,

@@ -298,3 +298,25 @@ def test_rows_without_columns(dev):
         pq.qcast_norm_per_token(e, w)
     with pytest.raises(pq.QcastError):
         pq.qcast_norm_backward_per_token(e, e, torch.ones(4, device=dev), w)
+
+
+@pytest.mark.parametrize("rows,cols,kind,ckpt", [(4099, 7168, "channel", "e4m3"), (4099, 7168, "token", None), (3001, 6400, "full", "e5m2"),
+                                                 (1701, 16384, "channel", "e4m3"), (1201, 16384, "full", None), (28001, 2048, None, None)])
+def test_large_inputs_row_for_row(dev, rows, cols, kind, ckpt):
+    """Inputs past the size that is read through the caches: every row as in a call on a few rows, bit for bit."""
+    g = torch.Generator(device=dev).manual_seed(rows)
+    bf16 = torch.bfloat16
+    y, h = (torch.randn(rows, cols, generator=g, device=dev).to(bf16) for _ in range(2))
+    wq, wp = (1 + 0.1 * torch.randn(cols, generator=g, device=dev)).to(bf16), torch.randn(cols, generator=g, device=dev).to(bf16)
+    gate = {None: None, "channel": wq + 1, "token": torch.randn(rows, generator=g, device=dev),
+            "full": torch.randn(rows, cols, generator=g, device=dev).to(bf16) if kind == "full" else None}[kind]
+    assert 2 * rows * cols * (3 if kind == "full" else 2) > 96 << 20
+    kw = dict(residual_scale=0.75, ckpt_fmt=ckpt)
+    whole = pq.qcast_norm_per_token(h, wq, y, wp, gate, **kw)
+    for r0 in list(range(0, rows, 1013)):
+        s = slice(r0, min(rows, r0 + 1013))
+        part = pq.qcast_norm_per_token(h[s], wq, y[s], wp, gate if kind in (None, "channel") else gate[s], **kw)
+        for name, a, b in zip(whole._fields, whole, part):
+            assert (a is None) == (b is None), name
+            if a is not None:
+                assert torch.equal(a[s].contiguous().view(torch.uint8), b.view(torch.uint8)), (name, r0)

@@ -406,7 +406,9 @@ QCAST_API int qcast_cast_back(const void* q, const float* sf, int64_t rows, int6
 /*
  * SwiGLU forward fused with the per-token cast and with an 8-bit checkpoint
  * of its input, for a backward pass that reads the checkpoint instead of h
- * (qcast_swiglu_backward_checkpoint): one read of h.
+ * (qcast_swiglu_backward_checkpoint_ex with ckpt_group = group, which needs
+ * cols % 128 == 0; qcast_cast_back reads the checkpoint of any cols): one
+ * read of h.
  *   h, row_weight, fmt, group, clamp_min, sf_flags, swiglu_clamp, q, sf: as
  *             qcast_swiglu_per_token_ex (nothing is counted). v comes from h
  *             itself, not from the checkpoint.
@@ -452,6 +454,18 @@ QCAST_API int qcast_swiglu_backward_checkpoint(
     const float* row_weight, int ckpt_fmt, int fmt, int group, float clamp_min, int sf_flags,
     float swiglu_clamp, void* q, void* sf, void* dhT, void* dhT_sf, void* vT, void* vT_sf,
     float* dw, void* ws, void* stream);
+
+/*
+ * qcast_swiglu_backward_checkpoint of a checkpoint with scale groups of
+ * ckpt_group (32, 64 or 128) elements, as qcast_swiglu_checkpoint writes it
+ * with that group: ckpt_sf [rows, 2*cols/ckpt_group]. Everything else, the
+ * groups of the outputs too, is the same.
+ */
+QCAST_API int qcast_swiglu_backward_checkpoint_ex(
+    const void* ckpt, const float* ckpt_sf, const void* dv, int64_t rows, int64_t cols,
+    const float* row_weight, int ckpt_fmt, int ckpt_group, int fmt, int group, float clamp_min,
+    int sf_flags, float swiglu_clamp, void* q, void* sf, void* dhT, void* dhT_sf, void* vT,
+    void* vT_sf, float* dw, void* ws, void* stream);
 
 /*
  * Stored per-token codes cast again along the tokens and written transposed:

@@ -40,7 +40,8 @@ __all__ = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_swiglu_per_token_noalloc", "qcast_per_block_sf", "qcast_per_channel_sf",
            "qcast_per_channel_T_sf", "qcast_swiglu_per_channel_T_sf",
            "qcast_swiglu_backward_per_token_sf", "qcast_swiglu_checkpoint",
-           "qcast_swiglu_backward_checkpoint", "qcast_recast_per_channel_T",
+           "qcast_swiglu_backward_checkpoint", "qcast_swiglu_backward_checkpoint_ex",
+           "qcast_recast_per_channel_T",
            "qcast_norm_per_token", "qcast_norm_backward_per_token", "SwigluGrad", "NormOut",
            "NormGrad", "sf_layout_shape", "SF_ROUND_POW2", "SF_COL_MAJOR",
            "SF_PACKED_UE8M0", "qcast_abi_version", "qcast_set_num_cus", "qcast_bench_copy",
@@ -605,12 +606,21 @@ def _like(t, shape, dtype, device, name):
     raise QcastError(2, f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
 
 
+def _stored_scales(sf, rows, cols, device, name):
+    """(group, pointer) of the scales ``[rows, cols/group]`` of stored codes."""
+    if not isinstance(sf, torch.Tensor) or sf.dim() != 2 or sf.shape[0] != rows or \
+            (sf.shape[1] == 0) != (cols == 0) or (cols and cols % sf.shape[1]):
+        raise QcastError(2, f"{name} must be a [rows, columns/g] tensor of {rows} rows")
+    return cols // sf.shape[1] if cols else 128, _like(sf, sf.shape, torch.float32, device, name)
+
+
 def qcast_swiglu_checkpoint(h, row_weight=None, fmt="e4m3", group=128, clamp_min=0.0, sf_flags=0,
                             swiglu_clamp=0.0, ckpt_fmt="e4m3", out=None, out_sf=None, ckpt=None,
                             ckpt_sf=None, stream=None):
     """SwiGLU of ``h [rows, 2N]`` cast per token, and the 8-bit per-token cast
-    of ``h`` itself for qcast_swiglu_backward_checkpoint: ``(out [rows, N],
-    out_sf, ckpt [rows, 2N], ckpt_sf [rows, 2N/group])``."""
+    of ``h`` itself, in the same groups, for qcast_swiglu_backward_checkpoint
+    (which needs N to be a multiple of 128): ``(out [rows, N], out_sf, ckpt
+    [rows, 2N], ckpt_sf [rows, 2N/group])``."""
     f, cf = fmt_id(fmt), fmt_id(ckpt_fmt)
     h, rows, cols = _gate_up(h)
     if cf not in (FMT_E4M3, FMT_E5M2):
@@ -636,8 +646,9 @@ def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4
                                      clamp_min=0.0, sf_flags=0, swiglu_clamp=0.0,
                                      transposed=True, weight_grad=True, stream=None):
     """SwiGLU backward from the 8-bit checkpoint ``ckpt [rows, 2N]`` (its format
-    is its dtype) with scales ``ckpt_sf [rows, 2N/128]``: a ``SwigluGrad`` of
-    ``dh [rows, 2N]`` codes of [dgate | dup] and ``dh_sf``; with ``transposed``
+    is its dtype) with scales ``ckpt_sf [rows, 2N/g]`` (g = 32, 64 or 128): a
+    ``SwigluGrad`` of ``dh [rows, 2N]`` codes of [dgate | dup] and ``dh_sf`` (in
+    groups of 128, as all the outputs); with ``transposed``
     ``dh_t [2N, rows_T]``, ``v_t [N, rows_T]`` and their scales, the operands of
     the weight gradients, rows_T = rows up to a multiple of 128 and the codes
     behind the last row zero; with ``weight_grad`` ``dw [rows]``, the gradient
@@ -651,7 +662,7 @@ def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4
         raise QcastError(4, "fmt must be an 8-bit format (e4m3 or e5m2)")
     cols = two_n // 2
     dev = ckpt.device
-    sfptr = _like(ckpt_sf, (rows, two_n // 128), torch.float32, dev, "ckpt_sf")
+    ckpt_group, sfptr = _stored_scales(ckpt_sf, rows, two_n, dev, "ckpt_sf")
     dvptr = _like(dv, (rows, cols), torch.bfloat16, dev, "dv")
     wptr = _row_weight(row_weight, rows, dev)
     rows_t = (rows + 127) // 128 * 128
@@ -671,11 +682,16 @@ def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4
             dw = _new((rows,), torch.float32)
             if cols > 128:
                 ws = _new((rows * (cols // 128),), torch.float32)
-        check(load().qcast_swiglu_backward_checkpoint(
-            ckpt.data_ptr(), sfptr, dvptr, rows, cols, wptr, cf, f, group, clamp_min, sf_flags,
-            swiglu_clamp, dh.data_ptr(), dh_sf.data_ptr(), _ptr(dh_t), _ptr(dh_t_sf), _ptr(v_t),
-            _ptr(v_t_sf), _ptr(dw), _ptr(ws), sh), "qcast_swiglu_backward_checkpoint")
+        check(load().qcast_swiglu_backward_checkpoint_ex(
+            ckpt.data_ptr(), sfptr, dvptr, rows, cols, wptr, cf, ckpt_group, f, group, clamp_min,
+            sf_flags, swiglu_clamp, dh.data_ptr(), dh_sf.data_ptr(), _ptr(dh_t), _ptr(dh_t_sf),
+            _ptr(v_t), _ptr(v_t_sf), _ptr(dw), _ptr(ws), sh), "qcast_swiglu_backward_checkpoint")
     return SwigluGrad(dh, dh_sf, dh_t, dh_t_sf, v_t, v_t_sf, dw)
+
+
+# the checkpoint's group comes from the scales' shape, so one function serves
+# both C entry points
+qcast_swiglu_backward_checkpoint_ex = qcast_swiglu_backward_checkpoint
 
 
 def qcast_recast_per_channel_T(q, sf, fmt="e4m3", group=128, clamp_min=0.0, sf_flags=0, out=None,
@@ -691,11 +707,7 @@ def qcast_recast_per_channel_T(q, sf, fmt="e4m3", group=128, clamp_min=0.0, sf_f
     if f not in (FMT_E4M3, FMT_E5M2):
         raise QcastError(4, "fmt must be an 8-bit format (e4m3 or e5m2)")
     dev = q.device
-    if not isinstance(sf, torch.Tensor) or sf.dim() != 2 or sf.shape[0] != rows or \
-            (sf.shape[1] == 0) != (cols == 0) or (cols and cols % sf.shape[1]):
-        raise QcastError(2, "sf must be a [rows, cols/g] tensor")
-    in_group = cols // sf.shape[1] if cols else 128
-    sfptr = _like(sf, sf.shape, torch.float32, dev, "sf")
+    in_group, sfptr = _stored_scales(sf, rows, cols, dev, "sf")
     rows_t = (rows + 127) // 128 * 128
     sh, ctx = _placed(dev, stream)
     with ctx:

@@ -85,6 +85,8 @@ def load():
                                     vp, vp],
         "qcast_swiglu_backward_checkpoint": [vp, vp, vp, i64, i64, vp, i32, i32, i32, f32, i32,
                                              f32] + [vp] * 9,
+        "qcast_swiglu_backward_checkpoint_ex": [vp, vp, vp, i64, i64, vp, i32, i32, i32, i32, f32,
+                                                i32, f32] + [vp] * 9,
         "qcast_recast_per_channel_T": [vp, vp, i64, i64, i32, i32, i32, i32, f32, i32, vp, vp,
                                        vp],
         "qcast_norm_per_token": [vp, vp, i64, i64, vp, vp, vp, i32, f32, f32, f32, i32, i32, f32,
@@ -127,7 +129,7 @@ EXPORTS = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_swiglu_per_token_noalloc", "qcast_per_block_sf", "qcast_per_channel_sf",
            "qcast_per_channel_T_sf", "qcast_swiglu_per_channel_T_sf",
            "qcast_swiglu_backward_per_token_sf", "qcast_swiglu_checkpoint",
-           "qcast_swiglu_backward_checkpoint", "qcast_recast_per_channel_T",
-           "qcast_norm_per_token", "qcast_norm_backward_per_token", "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
+           "qcast_swiglu_backward_checkpoint", "qcast_swiglu_backward_checkpoint_ex",
+           "qcast_recast_per_channel_T", "qcast_norm_per_token", "qcast_norm_backward_per_token", "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
            "qcast_bench_copy", "qcast_bench_check_scale", "qcast_bench_time_next",
            "qcast_bench_per_channel_T_traffic"]

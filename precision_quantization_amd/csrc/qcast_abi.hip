@@ -496,9 +496,20 @@ int qcast_swiglu_backward_checkpoint(const void* ckpt, const float* ckpt_sf, con
                                      int sf_flags, float swiglu_clamp, void* q, void* sf,
                                      void* dhT, void* dhT_sf, void* vT, void* vT_sf, float* dw,
                                      void* ws, void* stream) {
+  return qcast_swiglu_backward_checkpoint_ex(ckpt, ckpt_sf, dv, rows, cols, row_weight, ckpt_fmt,
+                                             128, fmt, group, clamp_min, sf_flags, swiglu_clamp,
+                                             q, sf, dhT, dhT_sf, vT, vT_sf, dw, ws, stream);
+}
+
+int qcast_swiglu_backward_checkpoint_ex(const void* ckpt, const float* ckpt_sf, const void* dv,
+                                        int64_t rows, int64_t cols, const float* row_weight,
+                                        int ckpt_fmt, int ckpt_group, int fmt, int group,
+                                        float clamp_min, int sf_flags, float swiglu_clamp,
+                                        void* q, void* sf, void* dhT, void* dhT_sf, void* vT,
+                                        void* vT_sf, float* dw, void* ws, void* stream) {
   if (!fp8_fmt(fmt) || !fp8_fmt(ckpt_fmt)) return QCAST_ERR_FORMAT;
   if (!sf_flags_ok(sf_flags)) return QCAST_ERR_FORMAT;
-  if (group != 128) return QCAST_ERR_GROUP;
+  if (group != 128 || !per_token_group_ok(ckpt_group)) return QCAST_ERR_GROUP;
   if (rows < 0 || cols < 0 || cols % 128 != 0 || too_big(rows, 2 * cols) ||
       !qcast::tile_fits(rows, cols, 2 * cols))
     return QCAST_ERR_SHAPE;
@@ -536,6 +547,7 @@ int qcast_swiglu_backward_checkpoint(const void* ckpt, const float* ckpt_sf, con
   p.ws = static_cast<float*>(ws);
   p.floor = floor_for(fmt, clamp_min);
   p.clamp = clamp_value(swiglu_clamp);
+  p.ckpt_shift = ckpt_group == 32 ? 2 : ckpt_group == 64 ? 3 : 4;
   p.rows = (uint32_t)rows;
   p.cols = (uint32_t)cols;
   return finish(qcast::launch_swiglu_backward_checkpoint(p, ckpt_fmt, fmt,

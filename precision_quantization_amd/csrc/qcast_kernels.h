@@ -151,7 +151,7 @@ struct TileCast {
 };
 struct SwigluTile {
   const uint8_t* ckpt;       // [rows, 2*cols] codes of (gate | up)
-  const float* ckpt_sf;      // [rows, 2*cols/128]
+  const float* ckpt_sf;      // [rows, 2*cols / (8 << ckpt_shift)]
   const uint16_t* dv;        // [rows, cols] bf16
   const float* w;            // [rows] or null
   uint8_t* q;                // [rows, 2*cols] codes of [dg | du]
@@ -162,6 +162,7 @@ struct SwigluTile {
   float* ws;                 // [cols/128][rows] partial sums of dw
   float floor;
   float clamp;               // 0: none
+  int ckpt_shift;            // log2(ckpt_group / 8)
   uint32_t rows, cols;
 };
 hipError_t launch_swiglu_backward_checkpoint(const SwigluTile& p, int ckpt_fmt, int fmt,

@@ -149,7 +149,8 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   const uint32_t ch = threadIdx.x & 15;          // 8-channel chunk
   const uint32_t quad = threadIdx.x >> 4;        // 4 tokens
   const uint32_t cols = p.cols;
-  const uint32_t gpr = cols / 64;                // checkpoint groups per row
+  const uint32_t gpr = cols / 64;                // groups of a row [dg | du]
+  const uint32_t cpr = (2 * cols) >> (p.ckpt_shift + 3);   // checkpoint groups of a row
 
   u32x2 graw[4], uraw[4];
   u32x4 draw[4];
@@ -158,7 +159,9 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
   const int left = (int)(p.rows - tq);           // of the lane's tokens, those that exist
   const uint8_t* cp = p.ckpt + (uint64_t)tq * 2 * cols + c0 + ch * 8;
   const uint16_t* dp = p.dv + (uint64_t)tq * cols + c0 + ch * 8;
-  const float* sp = p.ckpt_sf + (uint64_t)tq * gpr + ct;
+  // the lane's 8 channels lie in one group of 32, 64 or 128
+  const float* sp = p.ckpt_sf + (uint64_t)tq * cpr + (ct << (4 - p.ckpt_shift)) +
+                    (ch >> p.ckpt_shift);
   // plain loads: 32 us where the inputs are in the Infinity Cache (a gradient
   // that the product before has just written) against 41 with streaming
   // loads, and no slower from HBM (40.6 against 41.3; 8192 x 2048)
@@ -172,8 +175,8 @@ __global__ __launch_bounds__(kBlock, 4) void swiglu_backward_tile_kernel(SwigluT
       graw[i] = *reinterpret_cast<const u32x2*>(cp + i * 2 * cols);
       uraw[i] = *reinterpret_cast<const u32x2*>(cp + i * 2 * cols + cols);
       draw[i] = *reinterpret_cast<const u32x4*>(dp + i * cols);
-      gsf[i] = sp[i * gpr];
-      usf[i] = sp[i * gpr + gpr / 2];
+      gsf[i] = sp[i * cpr];
+      usf[i] = sp[i * cpr + cpr / 2];
       if (p.w) wr[i] = p.w[tq + i];
     }
   }

@@ -607,8 +607,11 @@ QCAST_API int qcast_abi_version(void);
  * The only grids sized by it are the capped ones of the counting SwiGLU casts
  * run without a count workspace (qcast_swiglu_per_token_ex and
  * qcast_swiglu_per_channel_T with clamp_count given, swiglu_clamp > 0 and
- * count_ws NULL); every other launch takes one workgroup per unit of work and
- * ignores it.
+ * count_ws NULL) and that of qcast_norm_per_token, whose workgroups walk the
+ * rows. qcast_norm_backward_per_token walks them too, but its grid, which
+ * fixes the order of its sums, follows from the sizes alone
+ * (qcast_norm_ws_rows); every other launch takes one workgroup per unit of
+ * work. These ignore it.
  */
 QCAST_API void qcast_set_num_cus(int n);
 

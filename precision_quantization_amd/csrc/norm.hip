@@ -45,7 +45,7 @@ namespace {
 // (measured with one row ahead, 4096 x 7168: 53 us against 56; without
 // checkpoints, where two fit in the registers, 44 against 46).
 constexpr unsigned kResidentWaves = 16;
-constexpr int64_t kComputeUnits = 256;
+constexpr int kMaxUnits = 4096;
 // Inputs of up to this many bytes are all read with plain loads: what of them
 // the 256 MB Infinity Cache still holds comes from there. Of larger ones, which
 // would push each other out, only y is, which the block has just written
@@ -258,7 +258,8 @@ auto pick(const NormForward& p) {
 
 }  // namespace
 
-hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream) {
+hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream,
+                       const LaunchCaps& caps) {
   if (rows == 0 || p.chunks == 0) return hipSuccess;
   if (rows >= (int64_t(1) << 31) || p.chunks > kNormMaxChunks) return hipErrorInvalidValue;
   const int inputs = 1 + (p.y != nullptr) + (p.gate_kind == kGateFull);
@@ -266,7 +267,9 @@ hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream) {
   const int kc = p.chunks > 1024 ? 2 : 1;
   const unsigned threads = (unsigned)(((p.chunks + kc - 1) / kc + 63) / 64 * 64);
   const unsigned waves = threads / 64;
-  const int64_t resident = kComputeUnits * (waves < kResidentWaves ? kResidentWaves / waves : 1);
+  // whatever the override says, row + 2 * grid stays within 32 bits
+  const int64_t cus = caps.num_cus < kMaxUnits ? caps.num_cus : kMaxUnits;
+  const int64_t resident = cus * (waves < kResidentWaves ? kResidentWaves / waves : 1);
   const unsigned grid = (unsigned)(rows < resident ? rows : resident);
   auto kernel = kc == 1 ? (cached ? pick<1, true>(p) : pick<1, false>(p))
                         : (cached ? pick<2, true>(p) : pick<2, false>(p));

@@ -610,7 +610,8 @@ int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t col
       !aligned(rstd_pre, 4) || !aligned(y_ckpt, 16) || !aligned(y_ckpt_sf, 4) ||
       !aligned(h_ckpt, 16) || !aligned(h_ckpt_sf, 4))
     return QCAST_ERR_ALIGN;
-  if (const int drc = device_ok()) return drc;
+  qcast::LaunchCaps caps;
+  if (const int crc = caps_for_current_device(&caps)) return crc;
   qcast::NormForward p{};
   p.y = static_cast<const uint16_t*>(y);
   p.h = static_cast<const uint16_t*>(h);
@@ -633,7 +634,7 @@ int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t col
   p.eps = eps;
   p.inv_n = 1.0f / (float)cols;
   p.chunks = (uint32_t)(cols / 8);
-  return finish(qcast::launch_norm(p, rows, static_cast<hipStream_t>(stream)));
+  return finish(qcast::launch_norm(p, rows, static_cast<hipStream_t>(stream), caps));
 }
 
 int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t rows, int64_t cols,

@@ -202,7 +202,8 @@ struct NormForward {
   float inv_n;               // 1 / cols
   uint32_t chunks;           // cols / 8
 };
-hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream);
+hipError_t launch_norm(const NormForward& p, int64_t rows, hipStream_t stream,
+                       const LaunchCaps& caps);
 
 struct NormBackward {
   const uint16_t* dx;

@@ -438,7 +438,8 @@ QCAST_API int qcast_swiglu_checkpoint(const void* h, int64_t rows, int64_t cols,
  *          writes a [rows_T, 2*cols] or [rows_T, cols] input with sf_flags
  *          (packed needs (rows_T/128) % 4 == 0, and 4 | cols/128).
  *   dw     [rows] fp32 or NULL: the gradient of row_weight,
- *          sum_j dv[r][j] * silu(g) * u (also when row_weight is NULL).
+ *          sum_j dv[r][j] * silu(g) * u (also when row_weight is NULL);
+ *          QCAST_ERR_SHAPE for rows without columns.
  *   ckpt   [rows, 2*cols] codes in ckpt_fmt (E4M3 or E5M2), ckpt_sf [rows,
  *          2*cols/128] fp32; dv [rows, cols] bf16; row_weight [rows] or NULL.
  *   fmt    QCAST_FMT_E4M3 or QCAST_FMT_E5M2; group must be 128;
@@ -532,7 +533,7 @@ typedef enum {
  *            range the factor 0, and one below fp32's normal numbers is not
  *            held to the accuracy of the rest.
  *   group 32, 64 or 128; cols % group == 0; cols <= QCAST_NORM_MAX_COLS;
- *   rows < 2^31. Every bf16 tensor and code output is 16-byte aligned.
+ *   rows < 2^31. With cols == 0 nothing is written, the factors included. Every bf16 tensor and code output is 16-byte aligned.
  */
 QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t cols,
                                    const void* w_post, const void* w_pre, const void* gate,
@@ -581,6 +582,7 @@ static inline int64_t qcast_norm_ws_rows(int64_t rows, int64_t cols) {
  *            least one of q (with sf) and dy_out is given.
  *   dw_pre, dw_post  [cols] fp32; dgate [cols] fp32, [rows] fp32 or [rows,
  *            cols] bf16 by gate_kind. Each may be NULL; all are overwritten.
+ *            A [rows] dgate of rows without columns is QCAST_ERR_SHAPE.
  *   ws       qcast_norm_ws_rows(rows, cols) * 2 * cols * 4 bytes of device
  *            memory (16-byte aligned; no particular contents) that no other
  *            call uses at the same time; may be NULL when rows is 0.

@@ -649,7 +649,8 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
   const int rc = check_norm(rows, cols, fmt, group, clamp_min, sf_flags, gate_kind,
                             residual_scale, weight_offset, saved_fmt);
   if (rc != QCAST_OK) return rc;
-  if (cols == 0) return QCAST_OK;
+  if (cols == 0)                                  // a token gate's sums over no columns
+    return rows > 0 && gate_kind == QCAST_GATE_TOKEN && dgate ? QCAST_ERR_SHAPE : QCAST_OK;
   const bool saved8 = saved_fmt != 0;
   if (rows > 0) {
     if (!dx || !saved_h || !rstd_pre || !w_pre || !dh_out || (saved8 && !saved_h_sf) ||

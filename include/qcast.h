@@ -533,7 +533,8 @@ typedef enum {
  *            range the factor 0, and one below fp32's normal numbers is not
  *            held to the accuracy of the rest.
  *   group 32, 64 or 128; cols % group == 0; cols <= QCAST_NORM_MAX_COLS;
- *   rows < 2^31. With cols == 0 nothing is written, the factors included. Every bf16 tensor and code output is 16-byte aligned.
+ *   rows < 2^31. Every bf16 tensor and code output is 16-byte aligned. With
+ *   cols == 0 nothing is written, the factors included.
  */
 QCAST_API int qcast_norm_per_token(const void* y, const void* h, int64_t rows, int64_t cols,
                                    const void* w_post, const void* w_pre, const void* gate,

@@ -546,13 +546,26 @@ NormOut = namedtuple("NormOut", "h out out_sf x rstd_post rstd_pre y_ckpt y_ckpt
                                 "h_ckpt_sf")
 NormGrad = namedtuple("NormGrad", "dh out out_sf dy dw_post dw_pre dgate")
 _HERE = nullcontext()
-try:
-    # what torch's generated code allocates with: 0.7 us a tensor, torch.empty 1.3;
-    # a small call's time is mostly its 4 to 9 outputs
-    _strided = torch._C._dynamo.guards._empty_strided_cuda
-except AttributeError:
-    def _strided(shape, strides, dtype):
-        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _torch_calls(c):
+    """(allocate on the current device, index of the current device, handle of
+    a device's current stream): what torch's generated code calls, from torch's
+    C module ``c``, where it has them, else the public functions. A small
+    call's time is mostly its 4 to 9 outputs: 0.7 us a tensor against 1.3 for
+    torch.empty, and a stream's handle 2 us less than a Stream object."""
+    try:
+        strided = c._dynamo.guards._empty_strided_cuda
+    except AttributeError:
+        def strided(shape, strides, dtype):
+            return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    here = getattr(c, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(c, "_cuda_getCurrentRawStream",
+                     lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return strided, here, stream
+
+
+_strided, _current_device, _current_stream = _torch_calls(torch._C)
 
 
 def _new(shape, dtype):
@@ -568,9 +581,9 @@ def _placed(device, stream):
     """The handle of the stream a call runs on and the context in which it
     allocates: outputs and workspaces come from that stream's pool, so memory
     still in use on the current stream is never handed to another one."""
-    here = torch._C._cuda_getDevice()
+    here = _current_device()
     if device.index == here:
-        current = torch._C._cuda_getCurrentRawStream(here)     # 2 us less than a Stream object
+        current = _current_stream(here)
     else:
         current = torch.cuda.current_stream(device).cuda_stream
     handle = current if stream is None else _stream(device, stream)

@@ -665,7 +665,8 @@ def qcast_swiglu_backward_checkpoint(ckpt, ckpt_sf, dv, row_weight=None, fmt="e4
     ``dh_t [2N, rows_T]``, ``v_t [N, rows_T]`` and their scales, the operands of
     the weight gradients, rows_T = rows up to a multiple of 128 and the codes
     behind the last row zero; with ``weight_grad`` ``dw [rows]``, the gradient
-    of ``row_weight``. What is not asked for is None."""
+    of ``row_weight`` (of a weight of 1 without one; past 128 columns it takes a
+    second launch). What is not asked for is None."""
     f = fmt_id(fmt)
     cf = _codes(ckpt, "ckpt")
     rows, two_n = ckpt.shape

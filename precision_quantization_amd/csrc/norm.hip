@@ -17,7 +17,8 @@
 // HBM bandwidth, or by the launch for a few rows. 4096 x 7168 with a channel
 // gate and both checkpoints: 48 us, 5.5 TB/s (a copy of as many bytes: 42.5;
 // with the barriers, the loads or the stores taken out 46, 44 or 47: its vector
-// instructions are the most of it); without checkpoints 37; one row 3.6.
+// instructions are the most of it); without checkpoints 37; one row 3.6; with
+// two chunks a lane 1024 x 16384 28 (a copy: 25).
 //
 // gfx950 design. A workgroup holds a row in registers from the load to the
 // last store (a lane kC chunks of 8 columns), so the row crosses HBM once
@@ -48,9 +49,14 @@ constexpr unsigned kResidentWaves = 16;
 constexpr int kMaxUnits = 4096;
 // Inputs of up to this many bytes are all read with plain loads: what of them
 // the 256 MB Infinity Cache still holds comes from there. Of larger ones, which
-// would push each other out, only y is, which the block has just written
-// (8192 x 2048, 67 MB: 26 us against 29, 16384 x 512, 34 MB: 14 against 17;
-// 4096 x 7168, 117 MB, inputs long unused: 50 against 49).
+// would push each other out, only y is, which the block has just written. What
+// the cache holds is not known here, so the rule goes by size. Plain against
+// streaming loads of h, in us: 8192 x 2048 (67 MB) with y and h just used 25.9
+// against 28.9, h alone 29.0 against 31.0, y alone 28.9 against 28.3, neither
+// 31.0 against 31.8; 16384 x 512 (34 MB) 13.5 against 15.4, 13.5 against 16.5,
+// 14.4 against 14.3, 18.2 against 17.6. It loses most with a cold elementwise
+// gate (16384 x 512, y just used: 20.2 against 17.7), and past the bound
+// (4096 x 7168, 117 MB, inputs long unused: 50 against 49).
 constexpr int64_t kCachedBytes = int64_t(96) << 20;
 constexpr int kMaxWaves = 16;
 

@@ -4,7 +4,9 @@
 // with the group size and the format chosen at run time.
 //
 // Decoding and encoding are the conversions of qcast_device.h; a decoded
-// value is the fp32 product code * sf, as cast_back forms it.
+// value is the fp32 product code * sf, as cast_back forms it (in the norm
+// backward code * (sf * r), r the row's factor 1 / sqrt(...): one rounding
+// placed otherwise).
 #pragma once
 
 #include "qcast_device.h"

@@ -12,8 +12,10 @@
 // per-token codes and 3 of transposed codes out. Per pair it also issues
 // about 42 vector instructions (an exponential, a reciprocal, five encodings
 // with their scalings and maxima): 22 us of the vector units' time for 8192 x
-// 2048, beside 25 us of a copy's for the bytes. Measured 32 us (29 without
-// dw's second launch); 40.6 when no input is in the Infinity Cache.
+// 2048, beside 25 us of a copy's for the bytes. Measured 31 to 32 us (29
+// without dw's second launch) with the inputs in the Infinity Cache; 39.7 with
+// none there, and 39.6 with dv just used and the checkpoint long unused, as in
+// a training step.
 //
 // gfx950 design. A workgroup of 512 owns 128 tokens x 128 channels of both
 // halves, so both directions' groups are whole inside it and each value is

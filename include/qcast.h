@@ -597,6 +597,171 @@ QCAST_API int qcast_norm_backward_per_token(
     int group, float clamp_min, int sf_flags, void* dh_out, void* q, void* sf, void* dy_out,
     float* dw_post, float* dw_pre, void* dgate, void* ws, void* stream);
 
+/*
+ * A mixture-of-experts layer around its products. A token goes to top_k
+ * experts; its slot k is the pair (token, k), slot number token * top_k + k.
+ * qcast_expert_sort gives every slot a row, the rows of one expert together;
+ * qcast_dispatch_* bring the tokens' rows there, qcast_combine brings the
+ * products' rows back, and qcast_combine_backward_per_token is its gradient
+ * (the gradient of a dispatch is the unweighted qcast_combine). For a few
+ * tokens qcast_matvec_e2m1 takes each slot's expert by itself: nothing is
+ * sorted. Shared limits: top_k <= QCAST_MAX_TOP_K, experts <=
+ * QCAST_MAX_EXPERTS, align a power of two <= QCAST_MAX_ALIGN, slots and rows
+ * < 2^31.
+ */
+#define QCAST_MAX_EXPERTS 1024
+#define QCAST_MAX_TOP_K 64
+#define QCAST_MAX_ALIGN 1024
+
+/* Rows that the sorted buffers of a layer have room for: every slot, and the
+ * rounding up of as many experts' runs as there can be. */
+static inline int64_t qcast_expert_rows(int64_t tokens, int64_t top_k, int64_t experts,
+                                        int64_t align) {
+  const int64_t slots = tokens * top_k;
+  const int64_t runs = experts < slots ? experts : slots;
+  return (slots + runs * (align - 1)) / align * align;
+}
+
+/* Slots that qcast_expert_sort gives to one workgroup, and the bytes of its
+ * workspace: the counts of each such part (0: none is needed). */
+static inline int64_t qcast_expert_sort_part(int64_t slots) {
+  const int64_t even = (slots + 255) / 256;
+  return even <= 4096 ? 4096 : (even + 1023) / 1024 * 1024;
+}
+static inline int64_t qcast_expert_sort_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
+  const int64_t slots = tokens * top_k, part = qcast_expert_sort_part(slots);
+  return slots <= part ? 0 : (slots + part - 1) / part * experts * 4;
+}
+
+/*
+ * Sort the slots of a batch by expert, in slot order within an expert.
+ *   ids      [tokens, top_k] int32 (id_bytes 4) or int64 (8). The experts
+ *            here are first .. first + experts - 1 (a rank's share); a slot
+ *            of any other id has no row.
+ *   counts   [experts]: slots of each. offsets [experts + 1]: the first row
+ *            of each expert's run; a run takes ceil(count / align) * align
+ *            rows, offsets[experts] is the end of the last.
+ *   dest     [tokens, top_k]: the row of each slot, or -1.
+ *   source   [qcast_expert_rows(...)]: the slot of each row; -1 for a run's
+ *            padding and behind the last run.
+ *   weight   [tokens, top_k] fp32 or NULL; row_weight [qcast_expert_rows(...)]
+ *            the same in row order (the row_weight of the SwiGLU casts), 0
+ *            where there is no slot. Both or neither.
+ *   ws       qcast_expert_sort_ws_bytes(...) of device memory (16-byte
+ *            aligned; no particular contents) that no other call uses at the
+ *            same time; may be NULL when that is 0.
+ *   experts >= 1. All outputs int32 and 4-byte aligned; all are overwritten.
+ *   With no slots counts and offsets are zeros.
+ */
+QCAST_API int qcast_expert_sort(const void* ids, int id_bytes, int64_t tokens, int64_t top_k,
+                                int64_t experts, int64_t first, int align, const float* weight,
+                                int32_t* dest, int32_t* source, int32_t* offsets, int32_t* counts,
+                                float* row_weight, void* ws, void* stream);
+
+/*
+ * Bring stored rows to their experts: row t of the input goes to the rows
+ * dest[t][0 .. top_k - 1] of the output.
+ *   in       [tokens, row_bytes] bytes: codes of any format, or bf16;
+ *            row_bytes % 16 == 0. out [rows, row_bytes].
+ *   sf_in    [tokens] rows of sf_words 4-byte words (fp32 scales or packed
+ *            UE8M0 words) in the layout of sf_flags_in, sf_out [rows] such
+ *            rows in that of sf_flags_out (qcast_sf_flags, of which only
+ *            QCAST_SF_COL_MAJOR counts: [sf_words][rows up to a multiple of
+ *            4]). Both NULL: no scales.
+ *   dest     [tokens, top_k]: distinct rows; a value outside [0, rows) is a
+ *            slot without a row, nothing is written for it.
+ *   offsets, counts  of qcast_expert_sort, experts and align as there: the
+ *            padding rows of each run are written as zeros, scales too. NULL
+ *            (both), or align 1: no padding.
+ *   Rows of out that are neither are left as they were. rows * sf_words <
+ *   2^31 and tokens * sf_words < 2^31.
+ */
+QCAST_API int qcast_dispatch_codes(const void* in, int64_t tokens, int64_t row_bytes,
+                                   const void* sf_in, int64_t sf_words, int sf_flags_in,
+                                   int64_t top_k, const int32_t* dest, const int32_t* offsets,
+                                   const int32_t* counts, int64_t experts, int align,
+                                   int64_t rows, void* out, void* sf_out, int sf_flags_out,
+                                   void* stream);
+
+/*
+ * qcast_dispatch_codes of the per-token cast of x: row dest[t][k] holds the
+ * codes and scales of x[t] (times weight[t][k], an fp32 product, when weight
+ * is not NULL), as qcast_per_token_sf writes them with fmt, group, clamp_min
+ * and sf_flags into a [rows, cols] output. Padding rows are the cast of zeros.
+ *   x        [tokens, cols] bf16; weight [tokens, top_k] fp32 or NULL.
+ */
+QCAST_API int qcast_dispatch_per_token(const void* x, int64_t tokens, int64_t cols, int64_t top_k,
+                                       const int32_t* dest, const float* weight,
+                                       const int32_t* offsets, const int32_t* counts,
+                                       int64_t experts, int align, int64_t rows, int fmt,
+                                       int group, float clamp_min, int sf_flags, void* q,
+                                       void* sf, void* stream);
+
+/*
+ * Bring the experts' rows back and sum them:
+ *   out[t] = base[t] + sum_k weight[t][k] * y[dest[t][k]]
+ * in fp32 from base on, k ascending, one rounding to bf16 at the end.
+ *   y        [rows, cols] bf16, cols % 8 == 0.
+ *   dest     [tokens, top_k] or NULL: slot s is row s (rows that were never
+ *            sorted). A value outside [0, rows) adds nothing, whatever its
+ *            weight.
+ *   weight   [tokens, top_k] fp32 or NULL (all ones); base, out [tokens,
+ *            cols] bf16, base NULL: zeros (a token without rows gives zeros).
+ */
+QCAST_API int qcast_combine(const void* y, int64_t rows, int64_t tokens, int64_t top_k,
+                            int64_t cols, const int32_t* dest, const float* weight,
+                            const void* base, void* out, void* stream);
+
+/*
+ * Gradient of qcast_combine, fused with the per-token cast of the experts'
+ * output gradient:
+ *   dy[dest[t][k]] = weight[t][k] * dout[t]
+ *   dw[t][k] = sum_j dout[t][j] * y[dest[t][k]][j]          (0 without a row)
+ * in fp32 (the gradient of base is dout itself).
+ *   dout     [tokens, cols] bf16; y [rows, cols] bf16, or NULL without dw.
+ *   q, sf    the cast of dy: fmt, group, clamp_min, sf_flags, [rows, cols],
+ *            as qcast_dispatch_per_token writes it, padding included; dy
+ *            [rows, cols] bf16, its padding rows zeros. Each may be NULL.
+ *   dw       [tokens, top_k] fp32 or NULL.
+ *   dest, weight, offsets, counts, experts, align as qcast_dispatch_per_token.
+ *   At least one of q, dy and dw is given. cols % group == 0.
+ */
+QCAST_API int qcast_combine_backward_per_token(
+    const void* dout, const void* y, int64_t tokens, int64_t cols, int64_t top_k,
+    const int32_t* dest, const float* weight, const int32_t* offsets, const int32_t* counts,
+    int64_t experts, int align, int64_t rows, int fmt, int group, float clamp_min, int sf_flags,
+    void* q, void* sf, void* dy, float* dw, void* stream);
+
+/*
+ * Products of a few rows with E2M1 weights:
+ *   out[r][i] = sum_j x[r / (rows / x_rows)][j] * W[ids[r]][i][j]
+ * where W = decode(w) * w_sf, summed in fp32 (in an order that the sizes and
+ * ids fix), rounded once to out_dtype.
+ *   w        [experts, n, k/2] codes as qcast_e2m1 writes them for the weights'
+ *            rows; w_sf [experts, n, k/w_group] fp32, or with
+ *            QCAST_SF_PACKED_UE8M0 in w_sf_flags its packed words [experts, n,
+ *            k/w_group/4] ((k/w_group) % 4 == 0). Other bits of w_sf_flags:
+ *            QCAST_SF_ROUND_POW2 changes nothing, QCAST_SF_COL_MAJOR is
+ *            QCAST_ERR_FORMAT.
+ *   ids      [rows] int32 (id_bytes 4) or int64 (8): each row's expert; a row
+ *            of an id outside [0, experts) is zeros. NULL: experts must be 1,
+ *            and every row takes it.
+ *   x        [x_rows, k], rows a multiple of x_rows (x_rows >= 1 when rows >
+ *            0): bf16 (x_fmt 0, x_sf NULL), or codes in x_fmt (E4M3 or E5M2)
+ *            with x_sf [x_rows, k/x_group] fp32.
+ *   w_group, x_group  32, 64 or 128; k % w_group == 0 (k % x_group == 0).
+ *   out      [rows, n] bf16 (QCAST_OUT_BF16) or fp32 (QCAST_OUT_F32). With
+ *            k == 0 it is zeros.
+ *   Made for up to some 64 rows an expert: more are taken 64 at a time, each
+ *   time reading the weights again.
+ *   Limits: rows, n < 2^31, k < 2^24.
+ */
+QCAST_API int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group,
+                                int64_t x_rows, const void* w, const void* w_sf, int w_group,
+                                int w_sf_flags, int64_t experts, const void* ids, int id_bytes,
+                                int64_t rows, int64_t n, int64_t k, int out_dtype, void* out,
+                                void* stream);
+
 /* Human-readable name of a status code (static string). */
 QCAST_API const char* qcast_status_str(int status);
 

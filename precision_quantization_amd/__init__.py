@@ -43,7 +43,9 @@ __all__ = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_swiglu_backward_checkpoint", "qcast_swiglu_backward_checkpoint_ex",
            "qcast_recast_per_channel_T",
            "qcast_norm_per_token", "qcast_norm_backward_per_token", "SwigluGrad", "NormOut",
-           "NormGrad", "sf_layout_shape", "SF_ROUND_POW2", "SF_COL_MAJOR",
+           "NormGrad", "qcast_expert_sort", "qcast_dispatch_codes", "qcast_dispatch_per_token",
+           "qcast_combine", "qcast_combine_backward_per_token", "qcast_matvec_e2m1", "ExpertPlan",
+           "CombineGrad", "expert_rows", "sf_layout_shape", "SF_ROUND_POW2", "SF_COL_MAJOR",
            "SF_PACKED_UE8M0", "qcast_abi_version", "qcast_set_num_cus", "qcast_bench_copy",
            "qcast_bench_check_scale", "qcast_bench_time_next",
            "qcast_bench_per_channel_T_traffic",
@@ -883,6 +885,270 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
             dw_pre.data_ptr(), _ptr(dgate), _ptr(ws), stream_handle),
             "qcast_norm_backward_per_token")
     return NormGrad(dh_out, out, out_sf, dy, dw_post, dw_pre, dgate)
+
+
+# ---- a mixture-of-experts layer around its products -------------------------
+
+ExpertPlan = namedtuple("ExpertPlan", "dest source offsets counts row_weight align")
+CombineGrad = namedtuple("CombineGrad", "out out_sf dy dw")
+
+
+def expert_rows(tokens, top_k, experts, align):
+    """Rows of the sorted buffers of a layer (``qcast_expert_rows`` of
+    include/qcast.h)."""
+    slots = tokens * top_k
+    return (slots + min(experts, slots) * (align - 1)) // align * align
+
+
+def _sort_parts(slots):
+    """Workgroups of qcast_expert_sort, each of which has a row of its
+    workspace (``qcast_expert_sort_ws_bytes`` of include/qcast.h)."""
+    even = (slots + 255) // 256
+    part = 4096 if even <= 4096 else (even + 1023) // 1024 * 1024
+    return 0 if slots <= part else (slots + part - 1) // part
+
+
+def _ids(ids, name, dim):
+    """An int32 or int64 index tensor: (pointer, bytes of an index)."""
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise QcastError(1, f"{name} must be a CUDA (HIP) tensor")
+    if ids.dtype not in (torch.int64, torch.int32) or ids.dim() != dim or not ids.is_contiguous():
+        raise QcastError(2, f"{name} must be a contiguous {dim}-D int32 or int64 tensor")
+    return ids.data_ptr(), 8 if ids.dtype == torch.int64 else 4
+
+
+def qcast_expert_sort(ids, experts, align=1, first=0, weight=None, stream=None):
+    """The slots of ``ids [tokens, top_k]`` (int32 or int64, as a router's
+    top-k gives them) sorted by expert (include/qcast.h): an ``ExpertPlan`` of
+    ``dest [tokens, top_k]``, ``source [rows]``, ``offsets [experts + 1]``,
+    ``counts [experts]`` (int32) and, with ``weight [tokens, top_k]`` (fp32),
+    ``row_weight [rows]``; rows = ``expert_rows(tokens, top_k, experts,
+    align)``. The experts here are ``first`` to ``first + experts - 1``; each
+    one's rows start at a multiple of ``align``."""
+    ptr, width = _ids(ids, "ids", 2)
+    tokens, top_k = ids.shape
+    experts, align = int(experts), int(align)
+    dev = ids.device
+    wptr = None if weight is None else _like(weight, (tokens, top_k), torch.float32, dev, "weight")
+    rows = expert_rows(tokens, top_k, experts, align) if align > 0 and experts > 0 else 0
+    parts = _sort_parts(tokens * top_k)
+    i32 = torch.int32
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        dest = _new((tokens, top_k), i32)
+        source = _new((rows,), i32)
+        offsets = _new((max(experts, 0) + 1,), i32)
+        counts = _new((max(experts, 0),), i32)
+        row_weight = None if wptr is None else _new((rows,), torch.float32)
+        ws = _new((parts * experts,), i32) if parts and experts > 0 else None
+        check(load().qcast_expert_sort(ptr, width, tokens, top_k, experts, first, align, wptr,
+                                       dest.data_ptr(), source.data_ptr(), offsets.data_ptr(),
+                                       counts.data_ptr(), _ptr(row_weight), _ptr(ws), sh),
+              "qcast_expert_sort")
+    return ExpertPlan(dest, source, offsets, counts, row_weight, align)
+
+
+def _plan(plan, tokens, device):
+    """(rows, top_k, experts, dest, offsets, counts) of a plan for `tokens`
+    tokens; the last three are pointers."""
+    i32 = torch.int32
+    dest, source, offsets, counts = plan.dest, plan.source, plan.offsets, plan.counts
+    if dest.dim() != 2 or source.dim() != 1 or counts.dim() != 1:
+        raise QcastError(2, "plan must hold dest [tokens, top_k], source [rows] and counts [experts]")
+    top_k, experts = dest.shape[1], counts.shape[0]
+    return (source.shape[0], top_k, experts, _like(dest, (tokens, top_k), i32, device, "plan.dest"),
+            _like(offsets, (experts + 1,), i32, device, "plan.offsets"),
+            _like(counts, (experts,), i32, device, "plan.counts"))
+
+
+def qcast_dispatch_codes(q, plan, sf=None, sf_flags=0, out_sf_flags=None, out=None, out_sf=None,
+                         stream=None):
+    """Rows of ``q [tokens, n]`` (codes of any format, or bf16; a row's bytes a
+    multiple of 16) and their scales ``sf`` brought to the rows of ``plan``:
+    ``(out [rows, n], out_sf)``. ``sf`` is float32 or int32 (packed UE8M0
+    words): ``[tokens, words]``, or with SF_COL_MAJOR in ``sf_flags`` ``[words,
+    tokens up to a multiple of 4]``; ``out_sf`` the same by ``out_sf_flags``
+    (None: as ``sf_flags``). A run's padding rows are zeros; rows behind the
+    last run are left as they were (new outputs: undefined)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise QcastError(1, "q must be a CUDA (HIP) tensor")
+    if q.dim() != 2 or not q.is_contiguous():
+        raise QcastError(2, "q must be a contiguous 2-D tensor")
+    tokens, n = q.shape
+    dev = q.device
+    rows, top_k, experts, dptr, optr, cptr = _plan(plan, tokens, dev)
+    out_sf_flags = sf_flags if out_sf_flags is None else out_sf_flags
+    words, sfptr, sf_shape = 0, None, None
+    if sf is not None:
+        if not isinstance(sf, torch.Tensor) or sf.dim() != 2 or \
+                sf.dtype not in (torch.float32, torch.int32):
+            raise QcastError(2, "sf must be a 2-D float32 or int32 tensor")
+        words = sf.shape[0] if sf_flags & SF_COL_MAJOR else sf.shape[1]
+        sfptr = _like(sf, (words, (tokens + 3) // 4 * 4) if sf_flags & SF_COL_MAJOR
+                      else (tokens, words), sf.dtype, dev, "sf")
+        sf_shape = (words, (rows + 3) // 4 * 4) if out_sf_flags & SF_COL_MAJOR else (rows, words)
+    elif out_sf is not None:
+        raise QcastError(1, "out_sf needs sf")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _new_out(out, (rows, n), q.dtype, dev, "out")
+        if sf is not None:
+            out_sf = _new_out(out_sf, sf_shape, sf.dtype, dev, "out_sf")
+        check(load().qcast_dispatch_codes(
+            q.data_ptr(), tokens, n * q.element_size(), sfptr, words, sf_flags, top_k, dptr, optr,
+            cptr, experts, plan.align, rows, out.data_ptr(), _ptr(out_sf), out_sf_flags, sh),
+            "qcast_dispatch_codes")
+    return out, out_sf
+
+
+def qcast_dispatch_per_token(x, plan, weight=None, fmt="e4m3", group=128, clamp_min=0.0,
+                             sf_flags=0, out=None, out_sf=None, stream=None):
+    """The per-token cast of bf16 ``x [tokens, cols]`` (times ``weight [tokens,
+    top_k]``, fp32) written to the rows of ``plan``: ``out [rows, cols]``,
+    ``out_sf`` of ``sf_layout_shape(rows, cols, group, sf_flags)``. A run's
+    padding rows are the cast of zeros; rows behind the last run are left as
+    they were (new outputs: undefined)."""
+    f = fmt_id(fmt)
+    x = _bf16_input(x, "x")
+    tokens, cols = x.shape
+    dev = x.device
+    rows, top_k, experts, dptr, optr, cptr = _plan(plan, tokens, dev)
+    wptr = None if weight is None else _like(weight, (tokens, top_k), torch.float32, dev, "weight")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _new_out(out, code_shape(f, rows, cols), _code_dtype(f), dev, "out")
+        shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
+        out_sf = _new_out(out_sf, shape, dt, dev, "out_sf")
+        check(load().qcast_dispatch_per_token(
+            x.data_ptr(), tokens, cols, top_k, dptr, wptr, optr, cptr, experts, plan.align, rows, f,
+            group, clamp_min, sf_flags, out.data_ptr(), out_sf.data_ptr(), sh),
+            "qcast_dispatch_per_token")
+    return out, out_sf
+
+
+def qcast_combine(y, dest=None, weight=None, base=None, top_k=None, out=None, stream=None):
+    """``base + sum_k weight[:, k] * y[dest[:, k]]`` as bf16 ``[tokens, cols]``
+    from the experts' outputs ``y [rows, cols]`` (bf16). ``dest [tokens,
+    top_k]``: int32 (an ``ExpertPlan``'s), -1 where there is no row; None:
+    ``y`` holds a token's ``top_k`` rows next to one another. ``weight
+    [tokens, top_k]`` fp32 (None: ones); ``base [tokens, cols]`` bf16 (None:
+    zeros). Without weight and base it is the gradient of a dispatch."""
+    y = _bf16_input(y, "y")
+    rows, cols = y.shape
+    dev = y.device
+    if dest is not None:
+        if not isinstance(dest, torch.Tensor) or dest.dim() != 2:
+            raise QcastError(2, "dest must be an int32 [tokens, top_k] tensor")
+        if top_k is not None and dest.shape[1] != top_k:
+            raise QcastError(2, f"dest has {dest.shape[1]} slots a token, not {top_k}")
+        tokens, top_k = dest.shape
+        dptr = _like(dest, (tokens, top_k), torch.int32, dev, "dest")
+    else:
+        if top_k is None or top_k < 1 or rows % top_k:
+            raise QcastError(2, "without dest, top_k must be given and divide y's rows")
+        tokens, dptr = rows // top_k, None
+    wptr = None if weight is None else _like(weight, (tokens, top_k), torch.float32, dev, "weight")
+    bptr = None if base is None else _like(base, (tokens, cols), torch.bfloat16, dev, "base")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _new_out(out, (tokens, cols), torch.bfloat16, dev, "out")
+        check(load().qcast_combine(y.data_ptr(), rows, tokens, top_k, cols, dptr, wptr, bptr,
+                                   out.data_ptr(), sh), "qcast_combine")
+    return out
+
+
+def qcast_combine_backward_per_token(dout, plan, y=None, weight=None, fmt="e4m3", group=128,
+                                     clamp_min=0.0, sf_flags=0, want_codes=True, want_dy=False,
+                                     out=None, out_sf=None, dy=None, stream=None):
+    """Gradient of qcast_combine over the rows of ``plan`` from ``dout [tokens,
+    cols]`` (bf16), fused with the per-token cast of the experts' output
+    gradient: a ``CombineGrad`` of ``out [rows, cols]``/``out_sf`` (with
+    ``want_codes``), the same in bf16 ``dy`` (with ``want_dy``) and, where
+    ``y`` (the forward's) is given, ``dw [tokens, top_k]`` fp32, the gradient
+    of ``weight``. Padding rows and rows behind the last run as
+    qcast_dispatch_per_token leaves them."""
+    f = fmt_id(fmt)
+    dout = _bf16_input(dout, "dout")
+    tokens, cols = dout.shape
+    dev = dout.device
+    rows, top_k, experts, dptr, optr, cptr = _plan(plan, tokens, dev)
+    yptr = None if y is None else _like(y, (rows, cols), torch.bfloat16, dev, "y")
+    wptr = None if weight is None else _like(weight, (tokens, top_k), torch.float32, dev, "weight")
+    if (out is not None or out_sf is not None) and not want_codes:
+        raise QcastError(1, "out and out_sf need want_codes")
+    if dy is not None and not want_dy:
+        raise QcastError(1, "dy needs want_dy")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        if want_codes:
+            out = _new_out(out, code_shape(f, rows, cols), _code_dtype(f), dev, "out")
+            shape, dt = sf_layout_shape(rows, cols, group if group > 0 else 1, sf_flags)
+            out_sf = _new_out(out_sf, shape, dt, dev, "out_sf")
+        if want_dy:
+            dy = _new_out(dy, (rows, cols), torch.bfloat16, dev, "dy")
+        dw = None if y is None else _new((tokens, top_k), torch.float32)
+        check(load().qcast_combine_backward_per_token(
+            dout.data_ptr(), yptr, tokens, cols, top_k, dptr, wptr, optr, cptr, experts,
+            plan.align, rows, f, group, clamp_min, sf_flags, _ptr(out), _ptr(out_sf), _ptr(dy),
+            _ptr(dw), sh), "qcast_combine_backward_per_token")
+    return CombineGrad(out, out_sf, dy, dw)
+
+
+def qcast_matvec_e2m1(x, w, w_sf, ids=None, x_sf=None, out_dtype=torch.bfloat16, out=None,
+                      stream=None):
+    """Products of a few rows with E2M1 weights: ``out [rows, n]`` (bf16 or
+    fp32), row r being ``W[ids[r]] @ x[r // (rows / x_rows)]``. ``w [experts,
+    n, k/2]`` (uint8, qcast_e2m1's codes of each weight) with scales ``w_sf
+    [experts, n, k/g]`` float32, or int32 packed UE8M0 words ``[experts, n,
+    k/g/4]``, g = 32, 64 or 128. ``ids``: int32 or int64, any shape, one row
+    each (zeros where outside the experts); None: one weight ``w [n, k/2]``
+    for every row of x. ``x [x_rows, k]``: bf16, or float8 codes with ``x_sf
+    [x_rows, k/g]``."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise QcastError(1, "x must be a CUDA (HIP) tensor")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise QcastError(2, "x must be a contiguous 2-D tensor")
+    x_rows, k = x.shape
+    dev = x.device
+    xf, xg, xsptr = 0, 128, None
+    if x_sf is not None:
+        xf = _codes(x, "x")
+        xg, xsptr = _stored_scales(x_sf, x_rows, k, dev, "x_sf")
+    elif x.dtype != torch.bfloat16:
+        raise QcastError(2, f"x must be bfloat16 (or float8 codes with x_sf), got {x.dtype}")
+    dims = 2 if ids is None else 3
+    if not isinstance(w, torch.Tensor) or w.dim() != dims or not isinstance(w_sf, torch.Tensor) or \
+            w_sf.dim() != dims:
+        raise QcastError(2, "w and w_sf must be [n, k/2] and [n, k/g] tensors, or with ids "
+                            "[experts, n, k/2] and [experts, n, k/g]")
+    experts, n = (1, w.shape[0]) if ids is None else w.shape[:2]
+    lead = tuple(w.shape[:-1])
+    wptr = _like(w, lead + (k // 2,), torch.uint8, dev, "w")
+    packed = w_sf.dtype == torch.int32
+    groups = w_sf.shape[-1] * (4 if packed else 1)
+    if (groups == 0) != (k == 0) or (k and k % groups):
+        raise QcastError(2, f"w_sf holds {groups} groups of a row of {k}")
+    wsptr = _like(w_sf, lead + (w_sf.shape[-1],), torch.int32 if packed else torch.float32, dev,
+                  "w_sf")
+    rows, iptr, width = x_rows, None, 8
+    if ids is not None:
+        if not isinstance(ids, torch.Tensor):
+            raise QcastError(1, "ids must be a CUDA (HIP) tensor")
+        iptr, width = _ids(ids, "ids", ids.dim())
+        rows = ids.numel()
+        if ids.device != dev:
+            raise QcastError(2, "ids must be on x's device")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise QcastError(4, "out_dtype must be torch.bfloat16 or torch.float32")
+    sh, ctx = _placed(dev, stream)
+    with ctx:
+        out = _new_out(out, (rows, n), out_dtype, dev, "out")
+        check(load().qcast_matvec_e2m1(
+            x.data_ptr(), xf, xsptr, xg, x_rows, wptr, wsptr, k // groups if k else 128,
+            SF_PACKED_UE8M0 if packed else 0, experts, iptr, width, rows, n, k,
+            OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, out.data_ptr(), sh),
+            "qcast_matvec_e2m1")
+    return out
 
 
 def qcast_abi_version():

@@ -93,6 +93,16 @@ def load():
                                  i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp],
         "qcast_norm_backward_per_token": [vp, vp, i64, i64, i32] + [vp] * 9 +
                                          [i32, f32, f32, i32, i32, f32, i32] + [vp] * 9,
+        "qcast_expert_sort": [vp, i32, i64, i64, i64, i64, i32] + [vp] * 8,
+        "qcast_dispatch_codes": [vp, i64, i64, vp, i64, i32, i64, vp, vp, vp, i64, i32, i64, vp,
+                                 vp, i32, vp],
+        "qcast_dispatch_per_token": [vp, i64, i64, i64, vp, vp, vp, vp, i64, i32, i64, i32, i32,
+                                     f32, i32, vp, vp, vp],
+        "qcast_combine": [vp, i64, i64, i64, i64, vp, vp, vp, vp, vp],
+        "qcast_combine_backward_per_token": [vp, vp, i64, i64, i64, vp, vp, vp, vp, i64, i32, i64,
+                                             i32, i32, f32, i32, vp, vp, vp, vp, vp],
+        "qcast_matvec_e2m1": [vp, i32, vp, i32, i64, vp, vp, i32, i32, i64, vp, i32, i64, i64,
+                              i64, i32, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -130,6 +140,9 @@ EXPORTS = ["qcast_per_token", "qcast_e2m1", "qcast_swiglu_per_token", "qcast_per
            "qcast_per_channel_T_sf", "qcast_swiglu_per_channel_T_sf",
            "qcast_swiglu_backward_per_token_sf", "qcast_swiglu_checkpoint",
            "qcast_swiglu_backward_checkpoint", "qcast_swiglu_backward_checkpoint_ex",
-           "qcast_recast_per_channel_T", "qcast_norm_per_token", "qcast_norm_backward_per_token", "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
+           "qcast_recast_per_channel_T", "qcast_norm_per_token", "qcast_norm_backward_per_token",
+           "qcast_expert_sort", "qcast_dispatch_codes", "qcast_dispatch_per_token", "qcast_combine",
+           "qcast_combine_backward_per_token", "qcast_matvec_e2m1",
+           "qcast_status_str", "qcast_abi_version", "qcast_set_num_cus",
            "qcast_bench_copy", "qcast_bench_check_scale", "qcast_bench_time_next",
            "qcast_bench_per_channel_T_traffic"]

@@ -1,0 +1,119 @@
+// dispatch.hip -- tokens' rows brought to the rows of their experts: stored
+// codes with their scales, or the per-token cast of bf16 rows.
+//
+// A row is read once and written top_k times: bound by HBM writes.
+//
+// gfx950 design. A wave takes one piece of a token's row (64 chunks of 16
+// bytes, or 512 columns to cast) and writes it to each of the token's rows,
+// whose numbers are the same in every lane. Workgroups behind the tokens'
+// write the padding of the runs.
+#include "qcast_runs.h"
+
+namespace qcast {
+namespace {
+
+constexpr uint32_t kWaves = kThreads / 64;
+
+__device__ __forceinline__ uint32_t scale_index(uint32_t row, uint32_t w, uint32_t words,
+                                                uint32_t pad) {
+  return pad ? w * pad + row : row * words + w;
+}
+
+// Pieces of a token: kSeg of 64 chunks each, then one for its scales.
+__global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes p, uint32_t pieces,
+                                                                  uint32_t groups) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t segs = (p.chunks + 63) / 64;
+  if (blockIdx.x >= groups) {
+    uint32_t r0, r1;
+    pad_range(p.runs, blockIdx.x - groups, r0, r1);
+    for (uint32_t r = r0; r < r1; ++r) {
+      for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads)
+        store_stream(p.out + (uint64_t)r * p.chunks + c, u32x4{0, 0, 0, 0});
+      if (p.sf_out)
+        for (uint32_t w = threadIdx.x; w < p.words; w += kThreads)
+          p.sf_out[scale_index(r, w, p.words, p.pad_out)] = 0;
+    }
+    return;
+  }
+  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / pieces));
+  const uint32_t piece = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % pieces));
+  if (t >= p.runs.tokens) return;
+  const int32_t* dest = p.runs.dest + (uint64_t)t * p.runs.top_k;
+  if (piece < segs) {
+    const uint32_t c = piece * 64 + lane;
+    if (c >= p.chunks) return;
+    const u32x4 v = p.in[(uint64_t)t * p.chunks + c];
+    for (uint32_t k = 0; k < p.runs.top_k; ++k) {
+      const uint32_t r = (uint32_t)dest[k];
+      if (r < p.runs.rows) store_stream(p.out + (uint64_t)r * p.chunks + c, v);
+    }
+  } else {
+    for (uint32_t w = lane; w < p.words; w += 64) {
+      const uint32_t v = p.sf_in[scale_index(t, w, p.words, p.pad_in)];
+      for (uint32_t k = 0; k < p.runs.top_k; ++k) {
+        const uint32_t r = (uint32_t)dest[k];
+        if (r < p.runs.rows) p.sf_out[scale_index(r, w, p.words, p.pad_out)] = v;
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p, uint32_t segs,
+                                                                 uint32_t groups) {
+  const uint32_t lane = threadIdx.x & 63;
+  if (blockIdx.x >= groups) {
+    uint32_t r0, r1;
+    pad_range(p.runs, blockIdx.x - groups, r0, r1);
+    const float zero[8] = {};
+    for (uint32_t r = r0; r < r1; ++r)
+      for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads)
+        cast_chunk(p.cast, r, c, p.chunks, zero);
+    return;
+  }
+  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / segs));
+  const uint32_t seg = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % segs));
+  const uint32_t c = seg * 64 + lane;
+  if (t >= p.runs.tokens || c >= p.chunks) return;      // a group's lanes leave together
+  const u32x4 raw = reinterpret_cast<const u32x4*>(p.x)[(uint64_t)t * p.chunks + c];
+  float x[8];
+  unpack8(raw, x);
+  const uint64_t slot = (uint64_t)t * p.runs.top_k;
+  for (uint32_t k = 0; k < p.runs.top_k; ++k) {
+    const uint32_t r = (uint32_t)p.runs.dest[slot + k];
+    if (r >= p.runs.rows) continue;
+    float v[8];
+    const float w = p.weight ? p.weight[slot + k] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p.weight ? w * x[i] : x[i];
+    cast_chunk(p.cast, r, c, p.chunks, v);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_dispatch_codes(const DispatchCodes& p, hipStream_t stream) {
+  const uint32_t pieces = (p.chunks + 63) / 64 + (p.sf_in ? 1 : 0);
+  const uint64_t groups = ((uint64_t)p.runs.tokens * pieces + kWaves - 1) / kWaves;
+  const uint64_t all = groups + pad_groups(p.runs);
+  if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
+  if (all == 0) return hipSuccess;
+  launch_kernel(dispatch_codes_kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, pieces,
+                (uint32_t)groups);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_cast(const DispatchCast& p, hipStream_t stream) {
+  const uint32_t segs = (p.chunks + 63) / 64;
+  const uint64_t groups = ((uint64_t)p.runs.tokens * segs + kWaves - 1) / kWaves;
+  const uint64_t all = groups + pad_groups(p.runs);
+  if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
+  if (all == 0) return hipSuccess;
+  launch_kernel(dispatch_cast_kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, segs,
+                (uint32_t)groups);
+  return hipGetLastError();
+}
+
+}  // namespace qcast

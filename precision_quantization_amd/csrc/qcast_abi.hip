@@ -184,6 +184,61 @@ int check_norm(int64_t rows, int64_t cols, int fmt, int group, float clamp_min, 
   return QCAST_OK;
 }
 
+constexpr int64_t kInt31 = (int64_t(1) << 31) - 1;
+
+bool align_ok(int align) {
+  return align >= 1 && align <= QCAST_MAX_ALIGN && (align & (align - 1)) == 0;
+}
+
+bool slots_ok(int64_t tokens, int64_t top_k) {
+  return tokens >= 0 && top_k >= 0 && top_k <= QCAST_MAX_TOP_K &&
+         (top_k == 0 || tokens <= kInt31 / top_k) && tokens <= kInt31;
+}
+
+// The sizes of the entry points that bring rows to their experts, a token
+// being `pieces` pieces of work.
+int check_runs(int64_t tokens, int64_t top_k, int64_t pieces, const int32_t* offsets,
+               const int32_t* counts, int64_t experts, int align, int64_t rows) {
+  if (!slots_ok(tokens, top_k) || rows < 0 || rows > kInt31 || tokens > kInt31 / pieces)
+    return QCAST_ERR_SHAPE;
+  if ((offsets != nullptr) != (counts != nullptr)) return QCAST_ERR_NULL;
+  if (offsets) {
+    if (experts < 1 || experts > QCAST_MAX_EXPERTS) return QCAST_ERR_SHAPE;
+    if (!align_ok(align)) return QCAST_ERR_VALUE;
+  }
+  return QCAST_OK;
+}
+
+qcast::ExpertRuns make_runs(int64_t tokens, int64_t top_k, const int32_t* dest,
+                            const int32_t* offsets, const int32_t* counts, int64_t experts,
+                            int align, int64_t rows) {
+  qcast::ExpertRuns r{};
+  r.dest = dest;
+  r.offsets = offsets;
+  r.counts = counts;
+  r.tokens = (uint32_t)tokens;
+  r.top_k = (uint32_t)top_k;
+  r.experts = offsets ? (uint32_t)experts : 0;
+  r.align = offsets ? (uint32_t)align : 1;
+  r.rows = (uint32_t)rows;
+  return r;
+}
+
+// The cast of the sorted rows.
+int check_row_cast(int64_t tokens, int64_t rows, int64_t cols, int fmt, int group,
+                   float clamp_min, int sf_flags) {
+  if (!any_fmt(fmt) || !sf_flags_ok(sf_flags)) return QCAST_ERR_FORMAT;
+  if (!per_token_group_ok(group)) return QCAST_ERR_GROUP;
+  if (rows < 0 || cols < 0 || cols % group != 0 || cols > kInt31 || too_big(rows, cols) ||
+      too_big(tokens, cols) || !sf_shape_ok(rows, cols, group, sf_flags))
+    return QCAST_ERR_SHAPE;
+  if (!clamp_min_ok(clamp_min)) return QCAST_ERR_VALUE;
+  return QCAST_OK;
+}
+
+// Pieces of 512 columns.
+int64_t column_pieces(int64_t cols) { return cols / 512 + 1; }
+
 }  // namespace
 
 extern "C" {
@@ -704,6 +759,214 @@ int qcast_norm_backward_per_token(const void* dx, const void* dh_in, int64_t row
   p.chunks = (uint32_t)(cols / 8);
   return finish(qcast::launch_norm_backward(p, rows, (uint32_t)qcast_norm_ws_rows(rows, cols),
                                             static_cast<hipStream_t>(stream)));
+}
+
+int qcast_expert_sort(const void* ids, int id_bytes, int64_t tokens, int64_t top_k,
+                      int64_t experts, int64_t first, int align, const float* weight,
+                      int32_t* dest, int32_t* source, int32_t* offsets, int32_t* counts,
+                      float* row_weight, void* ws, void* stream) {
+  if (!slots_ok(tokens, top_k) || experts < 1 || experts > QCAST_MAX_EXPERTS)
+    return QCAST_ERR_SHAPE;
+  if ((id_bytes != 4 && id_bytes != 8) || !align_ok(align)) return QCAST_ERR_VALUE;
+  const int64_t slots = tokens * top_k;
+  const int64_t rows = qcast_expert_rows(tokens, top_k, experts, align);
+  if (rows > kInt31) return QCAST_ERR_SHAPE;
+  if (!offsets || !counts) return QCAST_ERR_NULL;
+  if (slots > 0 && (!ids || !dest || !source || (weight != nullptr) != (row_weight != nullptr) ||
+                    (!ws && qcast_expert_sort_ws_bytes(tokens, top_k, experts) > 0)))
+    return QCAST_ERR_NULL;
+  if (!aligned(ids, (uintptr_t)id_bytes) || !aligned(weight, 4) || !aligned(dest, 4) ||
+      !aligned(source, 4) || !aligned(offsets, 4) || !aligned(counts, 4) ||
+      !aligned(row_weight, 4) || !aligned(ws, 16))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::ExpertSort p{};
+  p.ids = ids;
+  p.weight = weight;
+  p.dest = dest;
+  p.source = source;
+  p.offsets = offsets;
+  p.counts = counts;
+  p.row_weight = slots > 0 ? row_weight : nullptr;
+  p.ws = static_cast<int32_t*>(ws);
+  p.first = first;
+  p.slots = (uint32_t)slots;
+  p.rows = (uint32_t)rows;
+  p.experts = (uint32_t)experts;
+  p.align = (uint32_t)align;
+  p.part = (uint32_t)qcast_expert_sort_part(slots);
+  p.wide = id_bytes == 8;
+  return finish(qcast::launch_expert_sort(p, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_dispatch_codes(const void* in, int64_t tokens, int64_t row_bytes, const void* sf_in,
+                         int64_t sf_words, int sf_flags_in, int64_t top_k, const int32_t* dest,
+                         const int32_t* offsets, const int32_t* counts, int64_t experts,
+                         int align, int64_t rows, void* out, void* sf_out, int sf_flags_out,
+                         void* stream) {
+  if (!sf_flags_ok(sf_flags_in) || !sf_flags_ok(sf_flags_out)) return QCAST_ERR_FORMAT;
+  if (row_bytes < 0 || row_bytes % 16 != 0 || row_bytes > kInt31 || sf_words < 0 ||
+      sf_words > kInt31)
+    return QCAST_ERR_SHAPE;
+  if (const int rc = check_runs(tokens, top_k, row_bytes / 1024 + 2, offsets, counts, experts,
+                                align, rows))
+    return rc;
+  if (sf_words > 0 && (rows > kInt31 / sf_words || tokens > kInt31 / sf_words))
+    return QCAST_ERR_SHAPE;
+  if (tokens == 0 || top_k == 0 || rows == 0 || row_bytes == 0) return QCAST_OK;
+  if (!in || !out || !dest || (sf_in != nullptr) != (sf_out != nullptr)) return QCAST_ERR_NULL;
+  if (!aligned(in, 16) || !aligned(out, 16) || !aligned(sf_in, 4) || !aligned(sf_out, 4) ||
+      !aligned(dest, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  const bool scales = sf_in && sf_words > 0;
+  qcast::DispatchCodes p{};
+  p.runs = make_runs(tokens, top_k, dest, offsets, counts, experts, align, rows);
+  p.in = static_cast<const qcast::u32x4*>(in);
+  p.out = static_cast<qcast::u32x4*>(out);
+  p.sf_in = scales ? static_cast<const uint32_t*>(sf_in) : nullptr;
+  p.sf_out = scales ? static_cast<uint32_t*>(sf_out) : nullptr;
+  p.chunks = (uint32_t)(row_bytes / 16);
+  p.words = (uint32_t)sf_words;
+  p.pad_in = sf_flags_in & QCAST_SF_COL_MAJOR ? (uint32_t)((tokens + 3) / 4 * 4) : 0;
+  p.pad_out = sf_flags_out & QCAST_SF_COL_MAJOR ? (uint32_t)((rows + 3) / 4 * 4) : 0;
+  return finish(qcast::launch_dispatch_codes(p, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_dispatch_per_token(const void* x, int64_t tokens, int64_t cols, int64_t top_k,
+                             const int32_t* dest, const float* weight, const int32_t* offsets,
+                             const int32_t* counts, int64_t experts, int align, int64_t rows,
+                             int fmt, int group, float clamp_min, int sf_flags, void* q, void* sf,
+                             void* stream) {
+  if (const int rc = check_row_cast(tokens, rows, cols, fmt, group, clamp_min, sf_flags))
+    return rc;
+  if (const int rc = check_runs(tokens, top_k, column_pieces(cols), offsets, counts, experts,
+                                align, rows))
+    return rc;
+  if (tokens == 0 || top_k == 0 || rows == 0 || cols == 0) return QCAST_OK;
+  if (!x || !q || !sf || !dest) return QCAST_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 4) || !aligned(dest, 4) ||
+      !aligned(weight, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::DispatchCast p{};
+  p.runs = make_runs(tokens, top_k, dest, offsets, counts, experts, align, rows);
+  p.x = static_cast<const uint16_t*>(x);
+  p.weight = weight;
+  p.cast = qcast::make_row_cast(rows, cols, fmt, group, floor_for(fmt, clamp_min),
+                                (uint32_t)sf_flags, q, sf);
+  p.chunks = (uint32_t)(cols / 8);
+  return finish(qcast::launch_dispatch_cast(p, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_combine(const void* y, int64_t rows, int64_t tokens, int64_t top_k, int64_t cols,
+                  const int32_t* dest, const float* weight, const void* base, void* out,
+                  void* stream) {
+  if (cols < 0 || cols % 8 != 0 || cols > kInt31 || too_big(rows, cols) || too_big(tokens, cols))
+    return QCAST_ERR_SHAPE;
+  if (const int rc = check_runs(tokens, top_k, column_pieces(cols), nullptr, nullptr, 0, 1, rows))
+    return rc;
+  if (!dest && tokens * top_k > rows) return QCAST_ERR_SHAPE;
+  if (tokens == 0 || cols == 0) return QCAST_OK;
+  if (!out || (!y && rows > 0 && top_k > 0)) return QCAST_ERR_NULL;
+  if (!aligned(y, 16) || !aligned(base, 16) || !aligned(out, 16) || !aligned(dest, 4) ||
+      !aligned(weight, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::Combine p{};
+  p.y = static_cast<const uint16_t*>(y);
+  p.dest = dest;
+  p.weight = weight;
+  p.base = static_cast<const uint16_t*>(base);
+  p.out = static_cast<uint16_t*>(out);
+  p.rows = (uint32_t)rows;
+  p.tokens = (uint32_t)tokens;
+  p.top_k = (uint32_t)top_k;
+  p.chunks = (uint32_t)(cols / 8);
+  return finish(qcast::launch_combine(p, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_combine_backward_per_token(const void* dout, const void* y, int64_t tokens,
+                                     int64_t cols, int64_t top_k, const int32_t* dest,
+                                     const float* weight, const int32_t* offsets,
+                                     const int32_t* counts, int64_t experts, int align,
+                                     int64_t rows, int fmt, int group, float clamp_min,
+                                     int sf_flags, void* q, void* sf, void* dy, float* dw,
+                                     void* stream) {
+  if (const int rc = check_row_cast(tokens, rows, cols, fmt, group, clamp_min, sf_flags))
+    return rc;
+  if (const int rc = check_runs(tokens, top_k, column_pieces(cols), offsets, counts, experts,
+                                align, rows))
+    return rc;
+  if (tokens == 0 || top_k == 0) return QCAST_OK;
+  if (cols == 0) return dw ? QCAST_ERR_SHAPE : QCAST_OK;      // dw over no columns
+  if (!dout || !dest || (q != nullptr) != (sf != nullptr) || (!q && !dy && !dw) ||
+      (dw && !y && rows > 0))
+    return QCAST_ERR_NULL;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(sf, 4) ||
+      !aligned(dy, 16) || !aligned(dw, 4) || !aligned(dest, 4) || !aligned(weight, 4) ||
+      !aligned(offsets, 4) || !aligned(counts, 4))
+    return QCAST_ERR_ALIGN;
+  if (const int drc = device_ok()) return drc;
+  qcast::DispatchCast p{};
+  p.runs = make_runs(tokens, top_k, dest, offsets, counts, experts, align, rows);
+  p.x = static_cast<const uint16_t*>(dout);
+  p.weight = weight;
+  p.y = static_cast<const uint16_t*>(y);
+  p.dy = static_cast<uint16_t*>(dy);
+  p.dw = dw;
+  p.cast = qcast::make_row_cast(rows, cols, fmt, group, floor_for(fmt, clamp_min),
+                                (uint32_t)sf_flags, q, sf);
+  p.chunks = (uint32_t)(cols / 8);
+  return finish(qcast::launch_combine_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group, int64_t x_rows,
+                      const void* w, const void* w_sf, int w_group, int w_sf_flags,
+                      int64_t experts, const void* ids, int id_bytes, int64_t rows, int64_t n,
+                      int64_t k, int out_dtype, void* out, void* stream) {
+  if (x_fmt != 0 && !fp8_fmt(x_fmt)) return QCAST_ERR_FORMAT;
+  if (out_dtype != QCAST_OUT_BF16 && out_dtype != QCAST_OUT_F32) return QCAST_ERR_FORMAT;
+  if (!sf_flags_ok(w_sf_flags) || (w_sf_flags & QCAST_SF_COL_MAJOR)) return QCAST_ERR_FORMAT;
+  if (!per_token_group_ok(w_group) || (x_fmt != 0 && !per_token_group_ok(x_group)))
+    return QCAST_ERR_GROUP;
+  const bool packed = (w_sf_flags & QCAST_SF_PACKED_UE8M0) != 0;
+  if (rows < 0 || rows > kInt31 || x_rows < 0 || n < 0 || n > kInt31 || k < 0 ||
+      k >= (int64_t(1) << 24) || k % w_group != 0 || (x_fmt != 0 && k % x_group != 0) ||
+      (packed && (k / w_group) % 4 != 0) || experts < 0 || too_big(rows, n) ||
+      too_big(experts, n > 0 && k > 0 ? n * k : 1) || !qcast::matvec_fits(rows, n))
+    return QCAST_ERR_SHAPE;
+  if (rows > 0 && (x_rows == 0 || rows % x_rows != 0)) return QCAST_ERR_SHAPE;
+  if (!ids && experts != 1) return QCAST_ERR_SHAPE;
+  if (ids && id_bytes != 4 && id_bytes != 8) return QCAST_ERR_VALUE;
+  if (rows == 0 || n == 0) return QCAST_OK;
+  if (!out || (k > 0 && (!x || (x_fmt != 0) != (x_sf != nullptr) ||
+                         (experts > 0 && (!w || !w_sf)))))
+    return QCAST_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(x_sf, 4) || !aligned(w, 16) || !aligned(w_sf, 4) ||
+      !aligned(ids, (uintptr_t)(ids ? id_bytes : 4)) || !aligned(out, 16))
+    return QCAST_ERR_ALIGN;
+  qcast::LaunchCaps caps;
+  if (const int crc = caps_for_current_device(&caps)) return crc;
+  qcast::Matvec p{};
+  p.x = x;
+  p.x_sf = x_sf;
+  p.w = static_cast<const uint8_t*>(w);
+  p.w_sf = w_sf;
+  p.ids = ids;
+  p.out = out;
+  p.experts = experts;
+  p.x_fmt = x_fmt;
+  p.x_shift = x_group == 32 ? 0 : x_group == 64 ? 1 : 2;
+  p.w_shift = w_group == 32 ? 0 : w_group == 64 ? 1 : 2;
+  p.packed = packed;
+  p.wide = id_bytes == 8;
+  p.out_bf16 = out_dtype == QCAST_OUT_BF16;
+  p.rows = (uint32_t)rows;
+  p.x_rows = (uint32_t)x_rows;
+  p.n = (uint32_t)n;
+  p.k = (uint32_t)k;
+  return finish(qcast::launch_matvec(p, static_cast<hipStream_t>(stream), caps));
 }
 
 }  // extern "C"

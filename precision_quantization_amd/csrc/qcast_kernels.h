@@ -233,4 +233,81 @@ struct NormBackward {
 hipError_t launch_norm_backward(const NormBackward& p, int64_t rows, uint32_t parts,
                                 hipStream_t stream);
 
+// A mixture-of-experts layer's rows (expert_sort.hip, dispatch.hip, combine.hip).
+struct ExpertSort {
+  const void* ids;           // int32, or int64 when wide
+  const float* weight;       // or null, with row_weight
+  int32_t* dest;
+  int32_t* source;
+  int32_t* offsets;
+  int32_t* counts;
+  float* row_weight;
+  int32_t* ws;               // [parts][experts], null for one part
+  int64_t first;
+  uint32_t slots, rows, experts, align;
+  uint32_t part;             // slots of a workgroup
+  bool wide;
+};
+hipError_t launch_expert_sort(const ExpertSort& p, hipStream_t stream);
+
+// Where a token's slots go, and what of the output is padding.
+struct ExpertRuns {
+  const int32_t* dest;       // [tokens][top_k]
+  const int32_t* offsets;    // [experts + 1] or null: no padding
+  const int32_t* counts;     // [experts]
+  uint32_t tokens, top_k, experts, align, rows;
+};
+
+struct DispatchCodes {
+  ExpertRuns runs;
+  const u32x4* in;
+  u32x4* out;
+  const uint32_t* sf_in;     // or null
+  uint32_t* sf_out;
+  uint32_t chunks;           // 16-byte chunks of a row
+  uint32_t words;            // scale words of a row
+  uint32_t pad_in, pad_out;  // rows of a column-major layout; 0: row-major
+};
+hipError_t launch_dispatch_codes(const DispatchCodes& p, hipStream_t stream);
+
+// Rows of fp32 weight * x cast per token at their places.
+struct DispatchCast {
+  ExpertRuns runs;
+  const uint16_t* x;         // [tokens, cols]
+  const float* weight;       // [tokens, top_k] or null
+  const uint16_t* y;         // [rows, cols]; null without dw
+  uint16_t* dy;              // [rows, cols] bf16 or null
+  float* dw;                 // [tokens, top_k] or null
+  RowCast cast;              // q may be null
+  uint32_t chunks;           // cols / 8
+};
+hipError_t launch_dispatch_cast(const DispatchCast& p, hipStream_t stream);
+hipError_t launch_combine_backward(const DispatchCast& p, hipStream_t stream);
+
+struct Combine {
+  const uint16_t* y;
+  const int32_t* dest;       // or null: slot s is row s
+  const float* weight;       // or null
+  const uint16_t* base;      // or null
+  uint16_t* out;
+  uint32_t rows, tokens, top_k, chunks;
+};
+hipError_t launch_combine(const Combine& p, hipStream_t stream);
+
+// out[r][i] = sum_j x[r / per][j] * W[ids[r]][i][j] (matvec.hip).
+struct Matvec {
+  const void* x;             // bf16, or codes in x_fmt
+  const float* x_sf;
+  const uint8_t* w;
+  const void* w_sf;          // fp32, or packed words
+  const void* ids;           // or null
+  void* out;
+  int64_t experts;
+  int x_fmt, x_shift, w_shift;   // groups of 32 << shift
+  bool packed, wide, out_bf16;
+  uint32_t rows, x_rows, n, k;
+};
+bool matvec_fits(int64_t rows, int64_t n);
+hipError_t launch_matvec(const Matvec& p, hipStream_t stream, const LaunchCaps& caps);
+
 }  // namespace qcast

@@ -752,9 +752,10 @@ QCAST_API int qcast_combine_backward_per_token(
  *   w_group, x_group  32, 64 or 128; k % w_group == 0 (k % x_group == 0).
  *   out      [rows, n] bf16 (QCAST_OUT_BF16) or fp32 (QCAST_OUT_F32). With
  *            k == 0 it is zeros.
- *   Made for up to some 64 rows an expert: more are taken 64 at a time, each
+ *   Made for up to some 16 rows an expert: more are taken 16 at a time, each
  *   time reading the weights again.
- *   Limits: rows, n < 2^31, k < 2^24.
+ *   Limits: rows, n, experts < 2^31, k < 2^24, rows * n < 2^40, and fewer than 2^31
+ *   tiles of 16 columns of the rows' (or, where there are fewer, the) experts.
  */
 QCAST_API int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group,
                                 int64_t x_rows, const void* w, const void* w_sf, int w_group,

@@ -39,12 +39,6 @@ __device__ __forceinline__ uint64_t same_expert(uint32_t e, uint32_t experts) {
   return same;
 }
 
-// Orders the wave's own LDS accesses: what one lane wrote, another reads next.
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Count the slots [begin, end) of this wave into its column of `column`.
 __device__ __forceinline__ void count_wave(const ExpertSort& p, uint32_t begin, uint32_t end,
                                            uint32_t* column) {

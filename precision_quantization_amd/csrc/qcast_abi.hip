@@ -933,8 +933,8 @@ int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group, 
   const bool packed = (w_sf_flags & QCAST_SF_PACKED_UE8M0) != 0;
   if (rows < 0 || rows > kInt31 || x_rows < 0 || n < 0 || n > kInt31 || k < 0 ||
       k >= (int64_t(1) << 24) || k % w_group != 0 || (x_fmt != 0 && k % x_group != 0) ||
-      (packed && (k / w_group) % 4 != 0) || experts < 0 || too_big(rows, n) ||
-      too_big(experts, n > 0 && k > 0 ? n * k : 1) || !qcast::matvec_fits(rows, n))
+      (packed && (k / w_group) % 4 != 0) || experts < 0 || experts > kInt31 || too_big(rows, n) ||
+      too_big(experts, n > 0 && k > 0 ? n * k : 1) || !qcast::matvec_fits(rows, n, experts, ids != nullptr))
     return QCAST_ERR_SHAPE;
   if (rows > 0 && (x_rows == 0 || rows % x_rows != 0)) return QCAST_ERR_SHAPE;
   if (!ids && experts != 1) return QCAST_ERR_SHAPE;
@@ -946,8 +946,7 @@ int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group, 
   if (!aligned(x, 16) || !aligned(x_sf, 4) || !aligned(w, 16) || !aligned(w_sf, 4) ||
       !aligned(ids, (uintptr_t)(ids ? id_bytes : 4)) || !aligned(out, 16))
     return QCAST_ERR_ALIGN;
-  qcast::LaunchCaps caps;
-  if (const int crc = caps_for_current_device(&caps)) return crc;
+  if (const int drc = device_ok()) return drc;
   qcast::Matvec p{};
   p.x = x;
   p.x_sf = x_sf;
@@ -966,7 +965,7 @@ int qcast_matvec_e2m1(const void* x, int x_fmt, const float* x_sf, int x_group, 
   p.x_rows = (uint32_t)x_rows;
   p.n = (uint32_t)n;
   p.k = (uint32_t)k;
-  return finish(qcast::launch_matvec(p, static_cast<hipStream_t>(stream), caps));
+  return finish(qcast::launch_matvec(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

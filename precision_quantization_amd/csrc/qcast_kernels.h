@@ -307,7 +307,7 @@ struct Matvec {
   bool packed, wide, out_bf16;
   uint32_t rows, x_rows, n, k;
 };
-bool matvec_fits(int64_t rows, int64_t n);
-hipError_t launch_matvec(const Matvec& p, hipStream_t stream, const LaunchCaps& caps);
+bool matvec_fits(int64_t rows, int64_t n, int64_t experts, bool ids);
+hipError_t launch_matvec(const Matvec& p, hipStream_t stream);
 
 }  // namespace qcast

@@ -29,6 +29,12 @@ __device__ __forceinline__ u32x4 buffer_load16(RowBuffer b, uint32_t at) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, kPolicy);
 }
 
+// Orders the wave's own LDS accesses: what one lane wrote, another reads next.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Sums over the wave64: every lane ends with the same bits (each step adds a
 // pair of lanes' values, and fp32 addition commutes).
 template <int kCtrl>

@@ -625,8 +625,8 @@ static inline int64_t qcast_expert_rows(int64_t tokens, int64_t top_k, int64_t e
 /* Slots that qcast_expert_sort gives to one workgroup, and the bytes of its
  * workspace: the counts of each such part (0: none is needed). */
 static inline int64_t qcast_expert_sort_part(int64_t slots) {
-  const int64_t even = (slots + 255) / 256;
-  return even <= 4096 ? 4096 : (even + 1023) / 1024 * 1024;
+  const int64_t even = ((slots + 255) / 256 + 1023) / 1024 * 1024;
+  return slots <= 4096 ? 4096 : even < 2048 ? 2048 : even;
 }
 static inline int64_t qcast_expert_sort_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
   const int64_t slots = tokens * top_k, part = qcast_expert_sort_part(slots);

@@ -903,9 +903,10 @@ def expert_rows(tokens, top_k, experts, align):
 def _sort_parts(slots):
     """Workgroups of qcast_expert_sort, each of which has a row of its
     workspace (``qcast_expert_sort_ws_bytes`` of include/qcast.h)."""
-    even = (slots + 255) // 256
-    part = 4096 if even <= 4096 else (even + 1023) // 1024 * 1024
-    return 0 if slots <= part else (slots + part - 1) // part
+    if slots <= 4096:
+        return 0
+    part = max(2048, ((slots + 255) // 256 + 1023) // 1024 * 1024)
+    return (slots + part - 1) // part
 
 
 def _ids(ids, name, dim):

@@ -45,21 +45,29 @@ __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes 
     const uint32_t c = piece * 64 + lane;
     if (c >= p.chunks) return;
     const u32x4 v = p.in[(uint64_t)t * p.chunks + c];
-    for (uint32_t k = 0; k < p.runs.top_k; ++k) {
-      const uint32_t r = (uint32_t)dest[k];
-      if (r < p.runs.rows) store_stream(p.out + (uint64_t)r * p.chunks + c, v);
+    for (uint32_t k = 0; k < p.runs.top_k; k += kBatch) {
+      uint32_t r[kBatch];
+      slot_rows(dest, k, p.runs.top_k, r);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (r[j] < p.runs.rows) store_stream(p.out + (uint64_t)r[j] * p.chunks + c, v);
     }
   } else {
     for (uint32_t w = lane; w < p.words; w += 64) {
       const uint32_t v = p.sf_in[scale_index(t, w, p.words, p.pad_in)];
-      for (uint32_t k = 0; k < p.runs.top_k; ++k) {
-        const uint32_t r = (uint32_t)dest[k];
-        if (r < p.runs.rows) p.sf_out[scale_index(r, w, p.words, p.pad_out)] = v;
+      for (uint32_t k = 0; k < p.runs.top_k; k += kBatch) {
+        uint32_t r[kBatch];
+        slot_rows(dest, k, p.runs.top_k, r);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (r[j] < p.runs.rows) p.sf_out[scale_index(r[j], w, p.words, p.pad_out)] = v;
       }
     }
   }
 }
 
+// Without weights a row is cast once, whatever the number of its places.
+template <int kFmt, bool kWeighted>
 __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p, uint32_t segs,
                                                                  uint32_t groups) {
   const uint32_t lane = threadIdx.x & 63;
@@ -67,9 +75,13 @@ __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p,
     uint32_t r0, r1;
     pad_range(p.runs, blockIdx.x - groups, r0, r1);
     const float zero[8] = {};
-    for (uint32_t r = r0; r < r1; ++r)
-      for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads)
-        cast_chunk(p.cast, r, c, p.chunks, zero);
+    for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads) {
+      const ChunkScale s = chunk_scale<kFmt>(p.cast, c, zero);
+      for (uint32_t r = r0; r < r1; ++r) {
+        put_codes<kFmt>(p.cast, r, p.chunks, c, zero);
+        put_scale(p.cast, r, s);
+      }
+    }
     return;
   }
   const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
@@ -78,18 +90,39 @@ __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p,
   const uint32_t c = seg * 64 + lane;
   if (t >= p.runs.tokens || c >= p.chunks) return;      // a group's lanes leave together
   const u32x4 raw = reinterpret_cast<const u32x4*>(p.x)[(uint64_t)t * p.chunks + c];
-  float x[8];
+  float x[8], y[8];
   unpack8(raw, x);
-  const uint64_t slot = (uint64_t)t * p.runs.top_k;
-  for (uint32_t k = 0; k < p.runs.top_k; ++k) {
-    const uint32_t r = (uint32_t)p.runs.dest[slot + k];
-    if (r >= p.runs.rows) continue;
-    float v[8];
-    const float w = p.weight ? p.weight[slot + k] : 1.0f;
+  ChunkScale s;
+  if constexpr (!kWeighted) {
+    s = chunk_scale<kFmt>(p.cast, c, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p.weight ? w * x[i] : x[i];
-    cast_chunk(p.cast, r, c, p.chunks, v);
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * s.inv;
   }
+  const uint64_t slot = (uint64_t)t * p.runs.top_k;
+  for (uint32_t k = 0; k < p.runs.top_k; k += kBatch) {
+    uint32_t r[kBatch];
+    slot_rows(p.runs.dest + slot, k, p.runs.top_k, r);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (r[j] >= p.runs.rows) continue;
+      if constexpr (kWeighted) {
+        const float w = p.weight[slot + k + j];
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = w * x[i];
+        s = chunk_scale<kFmt>(p.cast, c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = v[i] * s.inv;
+      }
+      put_codes<kFmt>(p.cast, r[j], p.chunks, c, y);
+      put_scale(p.cast, r[j], s);
+    }
+  }
+}
+
+template <int kFmt>
+auto cast_kernel(bool weighted) {
+  return weighted ? dispatch_cast_kernel<kFmt, true> : dispatch_cast_kernel<kFmt, false>;
 }
 
 }  // namespace
@@ -111,7 +144,12 @@ hipError_t launch_dispatch_cast(const DispatchCast& p, hipStream_t stream) {
   const uint64_t all = groups + pad_groups(p.runs);
   if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
   if (all == 0) return hipSuccess;
-  launch_kernel(dispatch_cast_kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, segs,
+  const bool w = p.weight != nullptr;
+  auto kernel = p.cast.fmt == kE4M3   ? cast_kernel<kE4M3>(w)
+                : p.cast.fmt == kE5M2 ? cast_kernel<kE5M2>(w)
+                : p.cast.fmt == kE2M1 ? cast_kernel<kE2M1>(w)
+                                      : cast_kernel<kE5M6>(w);
+  launch_kernel(kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, segs,
                 (uint32_t)groups);
   return hipGetLastError();
 }

@@ -39,44 +39,57 @@ __device__ __forceinline__ uint64_t same_expert(uint32_t e, uint32_t experts) {
   return same;
 }
 
-// Count the slots [begin, end) of this wave into its column of `column`.
-__device__ __forceinline__ void count_wave(const ExpertSort& p, uint32_t begin, uint32_t end,
-                                           uint32_t* column) {
-  const uint32_t lane = threadIdx.x & 63;
-  for (uint32_t s = begin; s < end; s += 64) {
-    const uint32_t e = s + lane < end ? expert_of(p, s + lane) : p.experts;
-    const uint64_t same = same_expert(e, p.experts);
-    if (e < p.experts && (same & ((1ull << lane) - 1)) == 0)
-      column[e] += (uint32_t)__builtin_popcountll(same);
-    wave_order();
-  }
-}
-
+// The slots of a wave: [begin, end) of its workgroup's part.
 __device__ __forceinline__ void wave_slots(const ExpertSort& p, uint32_t& begin, uint32_t& end) {
   const uint32_t wave = threadIdx.x >> 6;
-  const uint32_t p0 = blockIdx.x * p.part;                     // < slots
+  const uint32_t p0 = blockIdx.x * p.part;
   const uint32_t p1 = p.slots - p0 < p.part ? p.slots : p0 + p.part;
   const uint32_t per = ((p1 - p0 + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   begin = p1 - p0 < wave * per ? p1 : p0 + wave * per;
   end = p1 - begin < per ? p1 : begin + per;
 }
 
+// Experts of a wave's slots, 64 at a time: the first kHeld times in registers,
+// asked for together; the rest (parts of more than 4096 slots) read again.
+constexpr int kHeld = 4;
+struct Slots {
+  uint32_t e[kHeld];
+  __device__ __forceinline__ void load(const ExpertSort& p, uint32_t begin, uint32_t end) {
+    const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const uint32_t s = begin + i * 64 + lane;
+      e[i] = s < end ? expert_of(p, s) : p.experts;
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(const ExpertSort& p, uint32_t begin, uint32_t end,
+                                       F&& f) const {
+    const uint32_t lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (begin + i * 64 < end) f(begin + i * 64 + lane, e[i]);
+    for (uint32_t s = begin + kHeld * 64; s < end; s += 64)
+      f(s + lane, s + lane < end ? expert_of(p, s + lane) : p.experts);
+  }
+};
+
 // The counts of one part (a workgroup's slots). kExperts: room in LDS.
 template <uint32_t kExperts>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(ExpertSort p) {
-  __shared__ uint32_t columns[kSortWaves][kExperts];
-  for (uint32_t i = threadIdx.x; i < kSortWaves * kExperts; i += kSortThreads)
-    (&columns[0][0])[i] = 0;
-  __syncthreads();
+  __shared__ uint32_t counts[kExperts];
   uint32_t begin, end;
   wave_slots(p, begin, end);
-  count_wave(p, begin, end, columns[threadIdx.x >> 6]);
+  Slots slots;
+  slots.load(p, begin, end);
+  for (uint32_t i = threadIdx.x; i < kExperts; i += kSortThreads) counts[i] = 0;
   __syncthreads();
-  if (threadIdx.x < p.experts) {
-    uint32_t n = 0;
-    for (uint32_t w = 0; w < kSortWaves; ++w) n += columns[w][threadIdx.x];
-    p.ws[blockIdx.x * p.experts + threadIdx.x] = (int32_t)n;
-  }
+  slots.each(p, begin, end, [&](uint32_t, uint32_t e) {
+    if (e < p.experts) atomicAdd(&counts[e], 1u);      // whole numbers: in any order the same
+  });
+  __syncthreads();
+  if (threadIdx.x < p.experts)
+    p.ws[blockIdx.x * p.experts + threadIdx.x] = (int32_t)counts[threadIdx.x];
 }
 
 // Rows without a slot.
@@ -87,74 +100,99 @@ __device__ __forceinline__ void no_slot(const ExpertSort& p, uint32_t row) {
 
 template <uint32_t kExperts>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(ExpertSort p) {
-  __shared__ uint32_t columns[kSortWaves][kExperts];
-  __shared__ uint32_t start[kExperts + 1];
-  __shared__ uint32_t sums[kSortWaves];
+  constexpr uint32_t kQ = kSortThreads / kExperts;     // threads of an expert
+  constexpr uint32_t kQWaves = kSortWaves / kQ;
+  __shared__ uint32_t columns[kSortWaves][kExperts];   // a wave's slots of each expert
+  __shared__ uint32_t sums[3][kQ][kExperts];           // of parts in all, of parts before, of waves
+  __shared__ uint32_t start[kExperts + 1], held[kExperts], wave_sums[kSortWaves];
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t e = threadIdx.x % kExperts, q = threadIdx.x / kExperts;
+  const bool mine = e < p.experts;
+  uint32_t begin = 0, end = 0;
+  if (p.slots) wave_slots(p, begin, end);
+  Slots slots;
+  slots.load(p, begin, end);
+  // thread (e, q): the slots of expert e in a kQ-th of the parts
+  uint32_t total = 0, before = 0;
+  if (p.ws && mine) {
+    const uint32_t b1 = gridDim.x * (q + 1) / kQ;
+    uint32_t b = gridDim.x * q / kQ;
+    for (; b + 8 <= b1; b += 8) {
+      uint32_t n[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = (uint32_t)p.ws[(b + i) * p.experts + e];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        total += n[i];
+        before += b + i < blockIdx.x ? n[i] : 0;
+      }
+    }
+    for (; b < b1; ++b) {
+      const uint32_t n = (uint32_t)p.ws[b * p.experts + e];
+      total += n;
+      before += b < blockIdx.x ? n : 0;
+    }
+  }
   for (uint32_t i = threadIdx.x; i < kSortWaves * kExperts; i += kSortThreads)
     (&columns[0][0])[i] = 0;
   __syncthreads();
-  uint32_t begin = 0, end = 0;
-  if (p.slots) wave_slots(p, begin, end);
   uint32_t* column = columns[wave];
-  count_wave(p, begin, end, column);
+  slots.each(p, begin, end, [&](uint32_t, uint32_t x) {
+    if (x < p.experts) atomicAdd(&column[x], 1u);
+  });
   __syncthreads();
-
-  // thread e: the slots of expert e before each wave, and in all
-  uint32_t total = 0, run = 0;
-  if (threadIdx.x < p.experts) {
-    uint32_t before = 0;
-    if (p.ws) {
-      for (uint32_t b = 0; b < gridDim.x; ++b) {
-        const uint32_t n = (uint32_t)p.ws[b * p.experts + threadIdx.x];
-        total += n;
-        before += b < blockIdx.x ? n : 0;
-      }
-    }
-    for (uint32_t w = 0; w < kSortWaves; ++w) {
-      const uint32_t n = columns[w][threadIdx.x];
-      columns[w][threadIdx.x] = before;
-      before += n;
-    }
-    if (!p.ws) total = before;
-    run = (total + p.align - 1) & ~(p.align - 1);
+  uint32_t in_waves = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kQWaves; ++w) in_waves += columns[q * kQWaves + w][e];
+  sums[0][q][e] = total;
+  sums[1][q][e] = before;
+  sums[2][q][e] = in_waves;
+  __syncthreads();
+  total = before = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < kQ; ++i) {
+    const uint32_t n = sums[2][i][e];
+    total += p.ws ? sums[0][i][e] : n;
+    before += sums[1][i][e] + (i < q ? n : 0);
+  }
+  // the slots of expert e before each of these waves
+#pragma unroll
+  for (uint32_t w = 0; w < kQWaves; ++w) {
+    const uint32_t n = columns[q * kQWaves + w][e];
+    columns[q * kQWaves + w][e] = before;
+    before += n;
   }
   // offsets: the sum of the runs before e, within the wave and over the waves
+  const uint32_t run = mine && q == 0 ? (total + p.align - 1) & ~(p.align - 1) : 0;
   uint32_t upto = run;
+#pragma unroll
   for (uint32_t d = 1; d < 64; d <<= 1) {
     const uint32_t v = (uint32_t)__shfl_up((int)upto, d);
     if (lane >= d) upto += v;
   }
-  if (lane == 63) sums[wave] = upto;
+  if (lane == 63) wave_sums[wave] = upto;
   __syncthreads();
-  uint32_t base = 0;
-  for (uint32_t w = 0; w < wave; ++w) base += sums[w];
-  if (threadIdx.x < p.experts) {
-    start[threadIdx.x] = base + upto - run;
-    if (threadIdx.x == p.experts - 1) start[p.experts] = base + upto;
+  if (mine && q == 0) {
+    uint32_t base = 0;
+    for (uint32_t w = 0; w < wave; ++w) base += wave_sums[w];
+    upto += base;
+    start[e] = upto - run;
+    held[e] = total;
+    if (e == p.experts - 1) start[p.experts] = upto;
     if (blockIdx.x == 0) {
-      p.counts[threadIdx.x] = (int32_t)total;
-      p.offsets[threadIdx.x] = (int32_t)(base + upto - run);
-      if (threadIdx.x == p.experts - 1) p.offsets[p.experts] = (int32_t)(base + upto);
+      p.counts[e] = (int32_t)total;
+      p.offsets[e] = (int32_t)(upto - run);
+      if (e == p.experts - 1) p.offsets[p.experts] = (int32_t)upto;
     }
-    // padding rows, the experts dealt to the workgroups
-    if (threadIdx.x % gridDim.x == blockIdx.x)
-      for (uint32_t r = base + upto - run + total; r < base + upto; ++r) no_slot(p, r);
   }
   __syncthreads();
-  for (uint32_t r = start[p.experts] + blockIdx.x * kSortThreads + threadIdx.x; r < p.rows;
-       r += gridDim.x * kSortThreads)
-    no_slot(p, r);
-
-  for (uint32_t s = begin; s < end; s += 64) {
-    const uint32_t slot = s + lane;
-    const uint32_t e = slot < end ? expert_of(p, slot) : p.experts;
-    const uint64_t same = same_expert(e, p.experts);
+  slots.each(p, begin, end, [&](uint32_t slot, uint32_t x) {
+    const uint64_t same = same_expert(x, p.experts);
     const uint64_t lower = same & ((1ull << lane) - 1);
-    if (e < p.experts) {
-      const uint32_t at = column[e];
-      const uint32_t row = start[e] + at + (uint32_t)__builtin_popcountll(lower);
-      if (lower == 0) column[e] = at + (uint32_t)__builtin_popcountll(same);
+    if (x < p.experts) {
+      const uint32_t at = column[x];
+      const uint32_t row = start[x] + at + (uint32_t)__builtin_popcountll(lower);
+      if (lower == 0) column[x] = at + (uint32_t)__builtin_popcountll(same);
       p.dest[slot] = (int32_t)row;
       p.source[row] = (int32_t)slot;
       if (p.row_weight) p.row_weight[row] = p.weight[slot];
@@ -162,7 +200,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(ExpertSort p) 
       p.dest[slot] = -1;
     }
     wave_order();
-  }
+  });
+  // padding rows, a wave for an expert, and the rows behind the last run
+  for (uint32_t x = blockIdx.x * kSortWaves + wave; x < p.experts; x += gridDim.x * kSortWaves)
+    for (uint32_t r = start[x] + held[x] + lane; r < start[x + 1]; r += 64) no_slot(p, r);
+  for (uint32_t r = start[p.experts] + blockIdx.x * kSortThreads + threadIdx.x; r < p.rows;
+       r += gridDim.x * kSortThreads)
+    no_slot(p, r);
 }
 
 template <uint32_t kExperts>

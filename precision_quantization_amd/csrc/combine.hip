@@ -58,12 +58,14 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t s
     store_stream(reinterpret_cast<u32x4*>(p.out) + (uint64_t)t * p.chunks + c, pack8_bf16(acc));
 }
 
-// A wave takes kSlots slots of one token over all columns, 512 at a time, the
-// next 512 asked for ahead. What is not asked for is a buffer of no bytes.
-constexpr int kSlots = 2;
+// A wave takes one slot over all columns, 512 at a time, with the next 512 asked
+// for ahead; the waves of a token's slots read its dout from the caches. What is
+// not asked for is a buffer of no bytes. 4096 x 8 x 7168 with codes and dw: 150
+// us (800 MB with the padding, 5.3 TB/s), as with two or four slots a wave (150
+// and 153), or a wave for 512 columns of all slots with a join of dw's parts
+// (151); 257 x 6 x 2048: 6.0, 6.4, 8.7 and 9.2.
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast p,
-                                                                    uint32_t pairs,
                                                                     uint32_t groups) {
   const uint32_t lane = threadIdx.x & 63;
   if (blockIdx.x >= groups) {
@@ -84,63 +86,44 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast
     }
     return;
   }
-  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / pairs));
-  const uint32_t k0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % pairs)) * kSlots;
-  if (t >= p.runs.tokens) return;
-  const uint32_t bytes = p.chunks * 16;
-  const uint64_t slot = (uint64_t)t * p.runs.top_k + k0;
-  uint32_t r[kSlots];
-  float w[kSlots], dot[kSlots];
-  RowBuffer y[kSlots];
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
-    const uint32_t s = k0 + j < p.runs.top_k ? j : 0;
-    r[j] = k0 + j < p.runs.top_k ? (uint32_t)p.runs.dest[slot + s] : kNoRow;
-    w[j] = p.weight ? p.weight[slot + s] : 1.0f;
-    const bool reads = r[j] < p.runs.rows && p.dw;
-    y[j] = row_buffer(p.y, reads ? (uint64_t)r[j] * bytes : 0, reads ? bytes : 0);
-    dot[j] = 0.0f;
+  const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(
+      (int)(blockIdx.x * kWaves + (threadIdx.x >> 6)));
+  if (slot >= p.runs.tokens * p.runs.top_k) return;
+  const uint32_t t = slot / p.runs.top_k, bytes = p.chunks * 16;
+  const uint32_t r = (uint32_t)p.runs.dest[slot];
+  if (r >= p.runs.rows) {
+    if (p.dw && lane == 0) p.dw[slot] = 0.0f;
+    return;
   }
+  const float w = p.weight ? p.weight[slot] : 1.0f;
   const RowBuffer x = row_buffer(p.x, (uint64_t)t * bytes, bytes);
-  u32x4 xn = buffer_load16<0>(x, lane * 16), yn[kSlots];
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) yn[j] = buffer_load16(y[j], lane * 16);
+  const RowBuffer y = row_buffer(p.y, p.dw ? (uint64_t)r * bytes : 0, p.dw ? bytes : 0);
+  float dot = 0.0f;
+  u32x4 xn = buffer_load16<0>(x, lane * 16), yn = buffer_load16(y, lane * 16);
   for (uint32_t c = lane; c - lane < p.chunks; c += 64) {
-    float d[8], f[kSlots][8];
+    float d[8], f[8], v[8];
     unpack8(xn, d);
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) unpack8(yn[j], f[j]);
+    unpack8(yn, f);
     xn = buffer_load16<0>(x, (c + 64) * 16);
+    yn = buffer_load16(y, (c + 64) * 16);
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) yn[j] = buffer_load16(y[j], (c + 64) * 16);
+    for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(d[i], f[i], dot);
+    if (c >= p.chunks) continue;                        // a group's lanes leave together
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int i = 0; i < 8; ++i) v[i] = w * d[i];
+    if (p.dy)
+      store_stream(reinterpret_cast<u32x4*>(p.dy) + (uint64_t)r * p.chunks + c, pack8_bf16(v));
+    if (p.cast.q) {
+      const ChunkScale s = chunk_scale<kFmt>(p.cast, c, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], f[j][i], dot[j]);
-      if (r[j] < p.runs.rows && c < p.chunks) {         // a group's lanes leave together
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = w[j] * d[i];
-        if (p.dy)
-          store_stream(reinterpret_cast<u32x4*>(p.dy) + (uint64_t)r[j] * p.chunks + c,
-                       pack8_bf16(v));
-        if (p.cast.q) {
-          const ChunkScale s = chunk_scale<kFmt>(p.cast, c, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = v[i] * s.inv;
-          put_codes<kFmt>(p.cast, r[j], p.chunks, c, v);
-          put_scale(p.cast, r[j], s);
-        }
-      }
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * s.inv;
+      put_codes<kFmt>(p.cast, r, p.chunks, c, v);
+      put_scale(p.cast, r, s);
     }
   }
   if (p.dw) {
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      const float sum = wave_sum(dot[j]);
-      if (lane == 0 && k0 + j < p.runs.top_k) p.dw[slot + j] = r[j] < p.runs.rows ? sum : 0.0f;
-    }
+    dot = wave_sum(dot);
+    if (lane == 0) p.dw[slot] = dot;
   }
 }
 
@@ -156,8 +139,7 @@ hipError_t launch_combine(const Combine& p, hipStream_t stream) {
 }
 
 hipError_t launch_combine_backward(const DispatchCast& p, hipStream_t stream) {
-  const uint32_t pairs = (p.runs.top_k + kSlots - 1) / kSlots;
-  const uint64_t groups = ((uint64_t)p.runs.tokens * pairs + kWaves - 1) / kWaves;
+  const uint64_t groups = ((uint64_t)p.runs.tokens * p.runs.top_k + kWaves - 1) / kWaves;
   const uint64_t all = groups + (p.cast.q || p.dy ? pad_groups(p.runs) : 0);
   if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
   if (all == 0) return hipSuccess;
@@ -165,8 +147,7 @@ hipError_t launch_combine_backward(const DispatchCast& p, hipStream_t stream) {
                 : p.cast.fmt == kE5M2 ? combine_backward_kernel<kE5M2>
                 : p.cast.fmt == kE2M1 ? combine_backward_kernel<kE2M1>
                                       : combine_backward_kernel<kE5M6>;
-  launch_kernel(kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, pairs,
-                (uint32_t)groups);
+  launch_kernel(kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, (uint32_t)groups);
   return hipGetLastError();
 }
 

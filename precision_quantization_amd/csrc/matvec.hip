@@ -19,12 +19,13 @@
 // A wave has a column tile and a share of its k, and asks for two turns of
 // weights and scales ahead; scales go through a piece of LDS that is the
 // wave's own (a lane that loaded its own row's scale of every step asked for
-// each of them four times: 3 us more on that weight). x is in LDS for the whole
-// workgroup, which then takes several column tiles, or, where it does not fit,
-// comes with the weights through the wave's own LDS, so that no wave waits for
-// another until those that share a tile add their sums, in a fixed order. Row 1
-// of 7168 x 18432 in groups of 32: 18.9 us (82.6 MB, 4.4 TB/s); 8 experts'
-// 4096 x 7168 in groups of 128: 26 us (4.8 TB/s).
+// each of them four times: 3 us more on that weight). The waves that share a
+// tile take its turns in turn and add their sums in a fixed order. x is in LDS
+// for the whole workgroup: all of it, or stages of it. Many rows without experts
+// bring theirs with the weights instead, through the wave's own LDS, so that no
+// wave waits for another. One row of 7168 x 18432 in groups of 32: 18.2 us (82.6
+// MB, 4.5 TB/s); 8 experts' 4096 x 7168 in groups of 128: 25.5 us (4.9 TB/s); 16
+// tokens to 8 of 32 experts of 7168 x 2048, groups of 32: 60 us (4.1 TB/s).
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -46,6 +47,7 @@ struct MatvecLaunch {
   uint32_t k_waves;      // waves that share a column tile
   uint32_t n_loop;       // column tiles that a wave takes one after the other
   uint32_t pass;         // rows that are taken at once
+  uint32_t x_lds;        // bytes of LDS for x
   uint32_t slots;        // 0: no ids
   bool by_row;           // a slot is a row (the first of its expert), else an expert
 };
@@ -107,52 +109,57 @@ __device__ __forceinline__ void lds_barrier() {
 enum XKind : int { kXPlain = 0, kXStep = 1, kXBlock = 2 };
 
 // A variant: the weights' scale groups (32 << kShift k, fp32 or packed), how x
-// comes, how many of its rows a pass takes at most (4 or 16), and whether all of
-// x is in LDS, for all waves, or comes with the weights, to each wave's own LDS.
-template <int kShift, bool kPacked, int kX, int kR, bool kAll>
+// comes, how many of its rows a pass takes at most (4 or 16), and where it is:
+// all of it in LDS for the workgroup, stages of it there, or with the weights,
+// through each wave's own LDS.
+enum XPlace : int { kWhole = 0, kStages = 1, kWithW = 2 };
+template <int kShift, bool kPacked, int kX, int kR, int kAt>
 struct Variant {
+  static constexpr bool kOwn = kAt == kWithW;
   static constexpr int kI = kR / 4;                    // results of a lane's four that hold rows
-  static constexpr int kUnits = kAll && kR == 4 ? 2 : 1;   // units of a turn
-  static constexpr int kAhead = !kAll && kX == kXStep ? 1 : 2;   // turns in flight
-  static constexpr int kWaves = kAll || kR == 4 ? 16 : 8;        // most waves of a workgroup
-  static constexpr int kTiles = kAll || kR == 4 ? 1 : 2;         // tiles of 16 columns that share x
+  static constexpr int kUnits = kR == 4 ? 2 : 1;       // units of a turn
+  static constexpr int kAhead = kOwn && kX == kXStep ? 1 : 2;    // turns in flight
+  static constexpr int kTiles = kOwn ? 2 : 1;          // tiles of 16 columns that share x
+  static constexpr int kWaves = kOwn ? 8 : 16;         // most waves of a workgroup
   static constexpr uint32_t kCols = 16 * kTiles;
   static constexpr int kGroups = kUnits * 8 >> kShift; // of a row of w, in a turn
   static constexpr int kPer = kGroups >= 4 ? kGroups / 4 : 1;   // of them, one lane's
-  static constexpr int kXLoads = kAll ? 1 : kX == kXPlain ? 2 * kI : kI;
-  static constexpr int kXScales = kX == kXPlain || kAll ? 1 : kX == kXBlock ? 2 : 8;   // of a unit
-  static constexpr int kSteps = kX == kXStep ? 8 : 2;  // scales of a unit of a row of x in LDS
-  static constexpr uint32_t kSfRow = kGroups * 4 + 16; // a row's scales of w in LDS
-  static constexpr uint32_t kXBytes = kAll ? 0 : kR * kXRow;
-  // a wave's LDS: its x, scales of w, and its sums of two tiles
-  static constexpr uint32_t kSums = kXBytes + 16 * kTiles * kSfRow;
+  static constexpr int kSteps = kX == kXPlain ? 0 : kX == kXStep ? 8 : 2;  // scales of a unit of x
+  static constexpr uint32_t kSfRow = kGroups * 4 + 16; // a row's scales in LDS
+  // a wave's LDS: its scales of w, its x, and its sums of two tiles
+  static constexpr uint32_t kXAt = 16 * kTiles * kSfRow;
+  static constexpr uint32_t kSums = kXAt + (kOwn ? kR * kXRow : 0);
   static constexpr uint32_t kLds = kSums + 2 * kTiles * kI * 256;
 
   // What a lane has in flight for one turn.
   struct Turn {
     u32x4 w[kUnits][kTiles][2];          // of rows lane % 8 and 8 more: chunk lane / 8
     uint32_t sf[kTiles][kPer];           // of row lane / 4, as stored (packed: a byte each)
-    u32x4 x[kXLoads];
-    float xs[kUnits][kI][kXScales];      // of the rows of the lane's results
+    // its own x: rows lane / 16 + 4 i, and the scales of the rows of its results
+    u32x4 x[!kOwn ? 1 : kX == kXPlain ? 2 * kI : kI];
+    float xs[kI][kOwn && kX != kXPlain ? kSteps : 1];
   };
 };
 
-// Where a wave reads. The 16 rows of a column tile are buffers: an offset past
-// their end (a row past n, a unit past the wave's last) loads zeros, so that
+// Where a wave reads. The rows of a column tile are buffers: an offset past
+// their end (a row past n, a unit past the last whole one) loads zeros, so that
 // the loads ahead need no branch and the compiler waits for no more than it
-// must. Units past the last read x's first bytes, and are not used.
+// must.
 constexpr uint32_t kPastEnd = 0x80000000u;
-template <int kI>
 struct Places {
   RowBuffer w, sf;
   uint32_t w_at, w_half, sf_at, sf_tile;
+  uint32_t end;                          // whole units
+};
+// Where its own x is.
+template <int kI>
+struct OwnRows {
   const uint8_t* x[kI];
-  const float* xs[kI];
-  uint32_t end;                          // of the wave's whole units
+  const float* s[kI];
 };
 
-template <typename V, int kShift, bool kPacked, int kX>
-__device__ __forceinline__ void load_turn_w(typename V::Turn& t, const Places<V::kI>& r,
+template <typename V, int kShift, bool kPacked>
+__device__ __forceinline__ void load_turn(typename V::Turn& t, const Places& r,
                                             uint32_t unit) {
 #pragma unroll
   for (int p = 0; p < V::kUnits; ++p) {
@@ -189,40 +196,9 @@ __device__ __forceinline__ void load_turn_w(typename V::Turn& t, const Places<V:
   }
 }
 
-template <typename V, int kX>
-__device__ __forceinline__ void load_turn_x(typename V::Turn& t, const Places<V::kI>& r,
-                                            uint32_t unit, uint32_t shift) {
-  const uint32_t lane = threadIdx.x & 63;
-  constexpr uint32_t kRowBytes = kX == kXPlain ? kUnit * 2 : kUnit;
-  const bool in = unit < r.end;
-  const uint32_t at = in ? unit * kRowBytes + (lane & 15) * 16 : 0;
-#pragma unroll
-  for (int i = 0; i < V::kI; ++i) {
-    if constexpr (kX == kXPlain) {
-      t.x[2 * i] = *reinterpret_cast<const u32x4*>(r.x[i] + at);
-      t.x[2 * i + 1] = *reinterpret_cast<const u32x4*>(r.x[i] + at + (in ? 256 : 0));
-    } else {
-      t.x[i] = *reinterpret_cast<const u32x4*>(r.x[i] + at);
-    }
-  }
-  if constexpr (kX != kXPlain) {
-#pragma unroll
-    for (int p = 0; p < V::kUnits; ++p)
-#pragma unroll
-      for (int i = 0; i < V::kI; ++i)
-#pragma unroll
-        for (int g = 0; g < V::kXScales; ++g) {
-          // scales of 128 k, or of 32 << shift k
-          const uint32_t u = unit + p;
-          const uint32_t j = kX == kXBlock ? u * 2 + g : (u * 8 + g) >> shift;
-          t.xs[p][i][g] = r.xs[i][u < r.end ? j : 0];
-        }
-  }
-}
-
 // The unit that k ends in, as the first unit of a turn: zeros past k.
-template <typename V, int kShift, bool kPacked, int kX>
-__device__ __forceinline__ void load_tail_w(typename V::Turn& t, const Places<V::kI>& r,
+template <typename V, int kShift, bool kPacked>
+__device__ __forceinline__ void load_tail(typename V::Turn& t, const Places& r,
                                             uint32_t k) {
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t unit = k / kUnit, k0 = unit * kUnit;
@@ -253,31 +229,6 @@ __device__ __forceinline__ void load_tail_w(typename V::Turn& t, const Places<V:
   }
 }
 
-template <typename V, int kX>
-__device__ __forceinline__ void load_tail_x(typename V::Turn& t, const Places<V::kI>& r,
-                                            uint32_t k, uint32_t shift) {
-  const uint32_t lane = threadIdx.x & 63, k0 = k / kUnit * kUnit;
-  // 8 (or, of codes, 16) k a lane
-#pragma unroll
-  for (int q = 0; q < V::kXLoads; ++q) {
-    constexpr bool kBf16 = kX == kXPlain;
-    const int i = kBf16 ? q / 2 : q;
-    const uint32_t at = kBf16 ? (q % 2) * 128 + (lane & 15) * 8 : (lane & 15) * 16;
-    t.x[q] = u32x4{0, 0, 0, 0};
-    if (k0 + at < k)
-      t.x[q] = *reinterpret_cast<const u32x4*>(r.x[i] + (k0 + at) * (kBf16 ? 2 : 1));
-  }
-  if constexpr (kX != kXPlain) {
-#pragma unroll
-    for (int i = 0; i < V::kI; ++i)
-#pragma unroll
-      for (int g = 0; g < V::kXScales; ++g) {
-        const uint32_t at = k0 + g * (kX == kXBlock ? 128 : 32);
-        t.xs[0][i][g] = at < k ? r.xs[i][at / 32 >> (kX == kXBlock ? 2 : shift)] : 0.0f;
-      }
-  }
-}
-
 // Eight 8-bit codes -> eight bf16 (exact).
 __device__ __forceinline__ u32x4 codes_bf16(uint32_t a, uint32_t b, int fmt) {
   float v[8];
@@ -291,28 +242,66 @@ __device__ __forceinline__ u32x4 codes_bf16(uint32_t a, uint32_t b, int fmt) {
   return pack8_bf16(v);
 }
 
-// The turn's x (as bf16) and scales (as fp32) to the wave's LDS.
-template <typename V, bool kPacked, int kX, bool kAll>
-__device__ __forceinline__ void store_turn(const typename V::Turn& t, uint8_t* mine, int fmt) {
-  const uint32_t lane = threadIdx.x & 63;
-  if constexpr (!kAll) {
-    uint8_t* to = mine + (lane >> 4) * kXRow + (lane & 15) * (kX == kXPlain ? 16 : 32);
+// A turn's own x (one unit). One past the last whole unit reads the rows' first
+// bytes, and is not used.
+template <typename V, int kX>
+__device__ __forceinline__ void load_own_x(typename V::Turn& t, const OwnRows<V::kI>& r,
+                                           uint32_t unit, uint32_t full, uint32_t shift) {
+  const uint32_t lane = threadIdx.x & 15;
+  const bool in = unit < full;
+  const uint32_t at = in ? unit * (kX == kXPlain ? kUnit * 2 : kUnit) + lane * 16 : 0;
 #pragma unroll
-    for (int i = 0; i < V::kI; ++i) {
-      if constexpr (kX == kXPlain) {
-        *reinterpret_cast<u32x4*>(to + i * 4 * kXRow) = t.x[2 * i];
-        *reinterpret_cast<u32x4*>(to + i * 4 * kXRow + 256) = t.x[2 * i + 1];
-      } else {
-        *reinterpret_cast<u32x4*>(to + i * 4 * kXRow) = codes_bf16(t.x[i].x, t.x[i].y, fmt);
-        *reinterpret_cast<u32x4*>(to + i * 4 * kXRow + 16) = codes_bf16(t.x[i].z, t.x[i].w, fmt);
+  for (int i = 0; i < V::kI; ++i) {
+    if constexpr (kX == kXPlain) {
+      t.x[2 * i] = *reinterpret_cast<const u32x4*>(r.x[i] + at);
+      t.x[2 * i + 1] = *reinterpret_cast<const u32x4*>(r.x[i] + at + (in ? 256 : 0));
+    } else {
+      t.x[i] = *reinterpret_cast<const u32x4*>(r.x[i] + at);
+#pragma unroll
+      for (int g = 0; g < V::kSteps; ++g) {
+        // scales of 128 k, or of 32 << shift k
+        const uint32_t j = kX == kXBlock ? unit * 2 + g : (unit * 8 + g) >> shift;
+        t.xs[i][g] = r.s[i][in ? j : 0];
       }
     }
   }
+}
+
+// The same of the unit that k ends in: zeros past k.
+template <typename V, int kX>
+__device__ __forceinline__ void load_own_tail(typename V::Turn& t, const OwnRows<V::kI>& r,
+                                              uint32_t k, uint32_t shift) {
+  const uint32_t lane = threadIdx.x & 15, k0 = k / kUnit * kUnit;
+#pragma unroll
+  for (int i = 0; i < V::kI; ++i) {
+    if constexpr (kX == kXPlain) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = k0 + h * 128 + lane * 8;
+        t.x[2 * i + h] = u32x4{0, 0, 0, 0};
+        if (at < k) t.x[2 * i + h] = *reinterpret_cast<const u32x4*>(r.x[i] + at * 2);
+      }
+    } else {
+      t.x[i] = u32x4{0, 0, 0, 0};
+      if (k0 + lane * 16 < k) t.x[i] = *reinterpret_cast<const u32x4*>(r.x[i] + k0 + lane * 16);
+#pragma unroll
+      for (int g = 0; g < V::kSteps; ++g) {
+        const uint32_t at = k0 + g * (kX == kXBlock ? 128 : 32);
+        t.xs[i][g] = at < k ? r.s[i][at / 32 >> (kX == kXBlock ? 2 : shift)] : 0.0f;
+      }
+    }
+  }
+}
+
+// The turn's scales of w to the wave's LDS, as fp32.
+template <typename V, bool kPacked>
+__device__ __forceinline__ void store_scales(const typename V::Turn& t, uint8_t* mine) {
+  const uint32_t lane = threadIdx.x & 63;
   constexpr int kParts = V::kGroups / V::kPer;
 #pragma unroll
   for (int t2 = 0; t2 < V::kTiles; ++t2) {
-    uint8_t* to = mine + V::kXBytes + (t2 * 16 + (lane >> 2)) * V::kSfRow +
-                  (lane & (kParts - 1)) * V::kPer * 4;
+    uint8_t* to =
+        mine + (t2 * 16 + (lane >> 2)) * V::kSfRow + (lane & (kParts - 1)) * V::kPer * 4;
     uint32_t f[V::kPer];
 #pragma unroll
     for (int g = 0; g < V::kPer; ++g)
@@ -323,13 +312,30 @@ __device__ __forceinline__ void store_turn(const typename V::Turn& t, uint8_t* m
   }
 }
 
-// All of x of the pass's cnt rows (row m in lane m of list), as bf16, rows of
-// `stride` bytes, zeros to the end of the last unit; and their scales, V::kSteps
-// of a unit, to `scales`. Four loads in flight.
+// The turn's own x to the wave's LDS, as bf16.
+template <typename V, int kX>
+__device__ __forceinline__ void store_own_x(const typename V::Turn& t, uint8_t* mine, int fmt) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint8_t* to = mine + V::kXAt + (lane >> 4) * kXRow + (lane & 15) * (kX == kXPlain ? 16 : 32);
+#pragma unroll
+  for (int i = 0; i < V::kI; ++i) {
+    if constexpr (kX == kXPlain) {
+      *reinterpret_cast<u32x4*>(to + i * 4 * kXRow) = t.x[2 * i];
+      *reinterpret_cast<u32x4*>(to + i * 4 * kXRow + 256) = t.x[2 * i + 1];
+    } else {
+      *reinterpret_cast<u32x4*>(to + i * 4 * kXRow) = codes_bf16(t.x[i].x, t.x[i].y, fmt);
+      *reinterpret_cast<u32x4*>(to + i * 4 * kXRow + 16) = codes_bf16(t.x[i].z, t.x[i].w, fmt);
+    }
+  }
+}
+
+// Units [u0, u0 + units) of x of the pass's cnt rows (row m in lane m of list),
+// as bf16, rows of `stride` bytes, zeros past k; and their scales, V::kSteps of
+// a unit, to rows of s_stride. Four loads in flight.
 template <typename V, int kX>
 __device__ __forceinline__ void stage_x(const Matvec& p, uint8_t* lds, float* scales,
-                                        uint32_t list, uint32_t cnt, uint32_t per,
-                                        uint32_t units, uint32_t stride) {
+                                        uint32_t list, uint32_t cnt, uint32_t per, uint32_t u0,
+                                        uint32_t units, uint32_t stride, uint32_t s_stride) {
   const uint32_t chunks = units * (kUnit / 8), all = cnt * chunks;
   constexpr int kBatch = 4;
   for (uint32_t i0 = threadIdx.x; i0 - (threadIdx.x & 63) < all; i0 += kBatch * blockDim.x) {
@@ -342,43 +348,43 @@ __device__ __forceinline__ void stage_x(const Matvec& p, uint8_t* lds, float* sc
       m[a] = i < all ? i / chunks : 0;
       j[a] = i - m[a] * chunks;
       const uint64_t x_row = (uint32_t)__shfl((int)list, (int)m[a]) / per;
+      const uint32_t at = u0 * kUnit + j[a] * 8;
       v[a] = u32x4{0, 0, 0, 0};
       sx[a] = 0.0f;
-      if (i < all && j[a] * 8 < p.k) {
+      if (i < all && at < p.k) {
         if constexpr (kX == kXPlain) {
           v[a] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) +
-                                                 x_row * p.k + j[a] * 8);
+                                                 x_row * p.k + at);
         } else {
           const u32x2 q = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p.x) +
-                                                          x_row * p.k + j[a] * 8);
+                                                          x_row * p.k + at);
           v[a].x = q.x;
           v[a].y = q.y;
-          sx[a] = p.x_sf[x_row * (p.k / 32 >> p.x_shift) + (j[a] / 4 >> p.x_shift)];
+          sx[a] = p.x_sf[x_row * (p.k / 32 >> p.x_shift) + (at / 32 >> p.x_shift)];
         }
       }
     }
 #pragma unroll
     for (int a = 0; a < kBatch; ++a) {
       if (i0 + a * blockDim.x < all) {
-        uint8_t* row = lds + m[a] * stride;
         if constexpr (kX != kXPlain) {
           constexpr uint32_t kOf = kUnit / 8 / V::kSteps;      // chunks of a scale
           v[a] = codes_bf16(v[a].x, v[a].y, p.x_fmt);
-          if (j[a] % kOf == 0) scales[m[a] * units * V::kSteps + j[a] / kOf] = sx[a];
+          if (j[a] % kOf == 0) scales[m[a] * s_stride + j[a] / kOf] = sx[a];
         }
-        *reinterpret_cast<u32x4*>(row + j[a] * 16) = v[a];
+        *reinterpret_cast<u32x4*>(lds + m[a] * stride + j[a] * 16) = v[a];
       }
     }
   }
 }
 
-template <int kShift, bool kPacked, int kX, int kR, bool kAll>
-__global__ __launch_bounds__((Variant<kShift, kPacked, kX, kR, kAll>::kWaves * 64)) void
-matvec_kernel(MatvecLaunch l) {
-  using V = Variant<kShift, kPacked, kX, kR, kAll>;
+template <int kShift, bool kPacked, int kX, int kR, int kAt>
+__global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(MatvecLaunch l) {
+  using V = Variant<kShift, kPacked, kX, kR, kAt>;
+  constexpr bool kOwn = V::kOwn;
   constexpr int kI = V::kI;
   const Matvec& p = l.p;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];    // the waves', then all of x
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];    // the waves', then x
   const uint32_t lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t wn = wave / l.k_waves, wk = wave - wn * l.k_waves;
@@ -396,50 +402,60 @@ matvec_kernel(MatvecLaunch l) {
   const bool none = expert < 0;                // the slot of rows that have no expert
 
   const uint32_t w_row = p.k / 2, sf_row = (p.k / (32 << kShift)) * (kPacked ? 1 : 4);
-  Places<kI> at;
+  Places at;
   at.w_at = (lane & 7) * w_row + (lane >> 3) * 16;
   at.w_half = 8 * w_row;
   at.sf_tile = 16 * sf_row;
   constexpr int kParts = V::kGroups / V::kPer;
   at.sf_at = (lane >> 2) * sf_row + (lane & (kParts - 1)) * V::kPer * (kPacked ? 1 : 4);
-  auto to_tile = [&](uint32_t tile) {
+  at.end = none ? 0 : p.k / kUnit;
+  auto to_tile = [&](Places& to, uint32_t tile) {
     const uint32_t held =
         tile * V::kCols >= p.n ? 0 : p.n - tile * V::kCols < V::kCols ? p.n - tile * V::kCols : V::kCols;
     const uint64_t row0 = held && !none ? (uint64_t)expert * p.n + tile * V::kCols : 0;
-    at.w = row_buffer(p.w, row0 * w_row, held * w_row);
-    at.sf = row_buffer(p.w_sf, row0 * sf_row, held * sf_row);
+    to.w = row_buffer(p.w, row0 * w_row, held * w_row);
+    to.sf = row_buffer(p.w_sf, row0 * sf_row, held * sf_row);
   };
-  // this wave's whole units of a tile, [begin, end), and its turns in all tiles
-  const uint32_t full = none ? 0 : p.k / kUnit;
-  const uint32_t begin = full * wk / l.k_waves;
-  at.end = full * (wk + 1) / l.k_waves;
-  const bool ends = !none && p.k % kUnit != 0 && wk == l.k_waves - 1;
-  const uint32_t turns = (at.end - begin + V::kUnits - 1) / V::kUnits;
+  // this wave's turns of a tile (wk, wk + k_waves, ...), and in all its tiles;
+  // with stages there is one tile
+  const uint32_t full = at.end;
+  const uint32_t all_turns = (full + V::kUnits - 1) / V::kUnits;
+  const uint32_t turns = wk < all_turns ? (all_turns - wk - 1) / l.k_waves + 1 : 0;
   const uint32_t items = turns * l.n_loop;
+  const bool ends = !none && p.k % kUnit != 0 && wk == l.k_waves - 1;
   const uint32_t per = l.slots ? p.rows / p.x_rows : 1;
   uint8_t* const mine = lds + wave * V::kLds;
-  uint8_t* const x_all = lds + l.n_waves * l.k_waves * V::kLds;
+  uint8_t* const x_lds = lds + l.n_waves * l.k_waves * V::kLds;
+  const uint8_t* const sa = mine + n * V::kSfRow;
   // A's row n is row m; rows that there are not give results that nobody reads
   const uint32_t m_of_lane = (n >> 2) + 4 * ((n & 3) % kI);
-  const uint32_t all_units = (p.k + kUnit - 1) / kUnit;
-  const uint32_t x_stride = kAll ? all_units * (kUnit * 2) + 16 : kXRow;
-  float* const x_scales = reinterpret_cast<float*>(x_all + l.pass * x_stride);
-  const uint8_t* const sa = mine + V::kXBytes + n * V::kSfRow;
 
-  // the ring; the next turn starts at unit `ahead` of tile `ahead_tile`
+  // the ring; the next turn that it asks for is `ahead` of tile `ahead_tile`
   typename V::Turn ring[V::kAhead];
-  uint32_t ahead = begin, ahead_tile = tile0;
+  OwnRows<kI> own;
+  uint32_t ahead = wk, ahead_tile = tile0;
   auto next = [&]() {
-    ahead += V::kUnits;
-    if (ahead >= at.end) {
-      ahead = begin;
+    ahead += l.k_waves;
+    if (ahead >= all_turns) {
+      ahead = wk;
       ++ahead_tile;
-      to_tile(ahead_tile < tile0 + l.n_loop ? ahead_tile : 0xfffffffu);
+      to_tile(at, ahead_tile < tile0 + l.n_loop ? ahead_tile : 0x7ffffffu);
     }
   };
-  // the first turn's weights are asked for before it is known whose rows they meet
-  to_tile(tile0);
-  if (items) load_turn_w<V, kShift, kPacked, kX>(ring[0], at, ahead);
+  auto begin = [&]() {
+    ahead = wk;
+    ahead_tile = tile0;
+    to_tile(at, tile0);
+#pragma unroll
+    for (int a = 0; a < V::kAhead; ++a) {
+      load_turn<V, kShift, kPacked>(ring[a], at, ahead * V::kUnits);
+      if constexpr (kOwn) load_own_x<V, kX>(ring[a], own, ahead * V::kUnits, full, p.x_shift);
+      next();
+    }
+  };
+  // without its own x the first weights are asked for before it is known whose
+  // rows they meet
+  if (!kOwn && items) begin();
   for (uint32_t first = 0;; first += l.pass) {
     // the rows of this pass: those with the slot's expert, l.pass at a time; lane
     // m holds the m-th
@@ -473,37 +489,51 @@ matvec_kernel(MatvecLaunch l) {
     }
     uint32_t row[kI];
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const uint32_t m = c + 4 * i;
-      row[i] = (uint32_t)__shfl((int)list, m < cnt ? (int)m : 0);
-      const uint64_t x_row = row[i] / per;
-      at.x[i] = static_cast<const uint8_t*>(p.x) + x_row * p.k * (kX == kXPlain ? 2 : 1);
-      at.xs[i] = p.x_sf + (kX == kXPlain ? 0 : x_row * (p.k / 32 >> p.x_shift));
+    for (int i = 0; i < kI; ++i)
+      row[i] = (uint32_t)__shfl((int)list, c + 4 * i < cnt ? (int)(c + 4 * i) : 0);
+
+    if constexpr (kOwn) {
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const uint64_t x_row = row[i] / per;
+        own.x[i] = static_cast<const uint8_t*>(p.x) + x_row * p.k * (kX == kXPlain ? 2 : 1);
+        own.s[i] = p.x_sf + (kX == kXPlain ? 0 : x_row * (p.k / 32 >> p.x_shift));
+      }
     }
 
-    if constexpr (kAll) {
-      if (!none) stage_x<V, kX>(p, x_all, x_scales, list, cnt, per, all_units, x_stride);
-      lds_barrier();
+    // x in LDS: all of it, or stages of as many units as fit, in whole rounds of
+    // the waves' rings (the launch sees to it that one fits)
+    const uint32_t units = none ? 0 : (p.k + kUnit - 1) / kUnit;
+    const uint32_t round = l.k_waves * V::kUnits * V::kAhead;
+    uint32_t stage = units;
+    if constexpr (kAt == kStages) {
+      const uint32_t most = (l.x_lds / cnt - 16) / (kUnit * 2 + V::kSteps * 4);
+      if (most < units) stage = most / round * round;
     }
-    const uint8_t* const xa =
-        (kAll ? x_all : mine) + (kAll && m_of_lane >= cnt ? 0 : m_of_lane) * x_stride + c * 16;
+    const uint32_t stride = kOwn ? kXRow : stage * (kUnit * 2) + 16, s_stride = stage * V::kSteps;
+    float* const scales = reinterpret_cast<float*>(x_lds + cnt * stride);
+    const uint8_t* const xa = (kOwn ? mine + V::kXAt : x_lds) +
+                              (kOwn || m_of_lane < cnt ? m_of_lane : 0) * stride + c * 16;
     const float* xs[kI];
 #pragma unroll
-    for (int i = 0; i < kI; ++i)
-      xs[i] = x_scales + (c + 4 * i < cnt ? c + 4 * i : 0) * all_units * V::kSteps;
+    for (int i = 0; i < kI; ++i) xs[i] = scales + (c + 4 * i < cnt ? c + 4 * i : 0) * s_stride;
+    uint32_t u0 = 0;                           // the first unit there now
 
     float acc[V::kTiles][kI];
 #pragma unroll
     for (int t2 = 0; t2 < V::kTiles; ++t2)
 #pragma unroll
       for (int i = 0; i < kI; ++i) acc[t2][i] = 0.0f;
-    auto add_turn = [&](const typename V::Turn& t, uint32_t unit, uint32_t held) {
-      store_turn<V, kPacked, kX, kAll>(t, mine, p.x_fmt);
+    // the units of a turn, `unit` on, that lie before `end`
+    auto add_turn = [&](const typename V::Turn& t, uint32_t unit, uint32_t end) {
+      store_scales<V, kPacked>(t, mine);
+      if constexpr (kOwn) store_own_x<V, kX>(t, mine, p.x_fmt);
       wave_order();
 #pragma unroll
       for (int u = 0; u < V::kUnits; ++u) {
-        if (u > 0 && u >= (int)held) break;
+        if (u > 0 && unit + u >= end) break;
         constexpr int kOfUnit = 8 >> kShift;
+        const uint32_t here = unit + u - (kAt == kStages ? u0 : 0);
         uint32_t r[V::kTiles][8];
 #pragma unroll
         for (int t2 = 0; t2 < V::kTiles; ++t2) to_steps(t.w[u][t2], r[t2]);
@@ -513,17 +543,17 @@ matvec_kernel(MatvecLaunch l) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             a[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
-                                                  xa + (kAll ? (unit + u) * (kUnit * 2) : 0) +
+                                                  xa + (kOwn ? 0 : here * (kUnit * 2)) +
                                                   h * 256 + j * 64));
-          float f_x[kI][kX == kXStep ? 4 : 1];
+          constexpr int kHalf = kX == kXStep ? 4 : 1;
+          float f_x[kI][kHalf];
           if constexpr (kX != kXPlain) {
-            constexpr int kHalf = kX == kXStep ? 4 : 1;
 #pragma unroll
             for (int i = 0; i < kI; ++i)
 #pragma unroll
               for (int g = 0; g < kHalf; ++g)
-                f_x[i][g] = kAll ? xs[i][(unit + u) * V::kSteps + h * kHalf + g]
-                                 : t.xs[u][i][kAll ? 0 : h * kHalf + g];
+                f_x[i][g] = kOwn ? t.xs[i][kOwn ? h * kHalf + g : 0]
+                                 : xs[i][here * V::kSteps + h * kHalf + g];
           }
           float s[V::kTiles][4 >> kShift];
 #pragma unroll
@@ -570,16 +600,12 @@ matvec_kernel(MatvecLaunch l) {
     uint32_t tile = tile0;
     auto flush = [&]() {
       if (ends) {
-        Places<kI> last = at;
-        const uint32_t held =
-            tile * V::kCols >= p.n ? 0 : p.n - tile * V::kCols < V::kCols ? p.n - tile * V::kCols : V::kCols;
-        const uint64_t row0 = held ? (uint64_t)expert * p.n + tile * V::kCols : 0;
-        last.w = row_buffer(p.w, row0 * w_row, held * w_row);
-        last.sf = row_buffer(p.w_sf, row0 * sf_row, held * sf_row);
+        Places last = at;
+        to_tile(last, tile);
         typename V::Turn t;
-        load_tail_w<V, kShift, kPacked, kX>(t, last, p.k);
-        if constexpr (!kAll) load_tail_x<V, kX>(t, last, p.k, p.x_shift);
-        add_turn(t, full, 1);
+        load_tail<V, kShift, kPacked>(t, last, p.k);
+        if constexpr (kOwn) load_own_tail<V, kX>(t, own, p.k, p.x_shift);
+        add_turn(t, full, full + 1);
       }
       const uint32_t half = (tile - tile0) & 1;
       if (l.k_waves > 1) {
@@ -587,8 +613,9 @@ matvec_kernel(MatvecLaunch l) {
 #pragma unroll
           for (int t2 = 0; t2 < V::kTiles; ++t2)
 #pragma unroll
-            for (int i = 0; i < kI; ++i) reinterpret_cast<float*>(mine + V::kSums)[((half * V::kTiles + t2) * kI + i) * 64 + lane] =
-                  acc[t2][i];
+            for (int i = 0; i < kI; ++i)
+              reinterpret_cast<float*>(mine + V::kSums)[((half * V::kTiles + t2) * kI + i) * 64 +
+                                                        lane] = acc[t2][i];
         }
         lds_barrier();
       }
@@ -623,78 +650,144 @@ matvec_kernel(MatvecLaunch l) {
         for (int i = 0; i < kI; ++i) acc[t2][i] = 0.0f;
       ++tile;
     };
-    if (items) {
-      if (first) {
-        ahead = begin;
-        ahead_tile = tile0;
-        to_tile(tile0);
-        load_turn_w<V, kShift, kPacked, kX>(ring[0], at, ahead);
-      }
-      if constexpr (!kAll) load_turn_x<V, kX>(ring[0], at, ahead, p.x_shift);
+    if (items && (kOwn || first)) begin();
+    // a turn, and the one that takes its place in the ring; places are fixed, so
+    // that nothing waits for a load but its use
+    uint32_t turn = wk;
+    auto refill = [&](typename V::Turn& t) {
+      load_turn<V, kShift, kPacked>(t, at, ahead * V::kUnits);
+      if constexpr (kOwn) load_own_x<V, kX>(t, own, ahead * V::kUnits, full, p.x_shift);
       next();
+    };
+    if constexpr (kAt == kStages) {
+      for (uint32_t held = 0; u0 < units; u0 += held) {
+        held = units - u0 < stage ? units - u0 : stage;
+        if (u0) lds_barrier();                 // the last units have been read
+        stage_x<V, kX>(p, x_lds, scales, list, cnt, per, u0, held, stride, s_stride);
+        lds_barrier();
+        const uint32_t end = u0 + held < units ? (u0 + held) / V::kUnits : all_turns;
+        while (turn < end) {
 #pragma unroll
-      for (int a = 1; a < V::kAhead; ++a) {
-        load_turn_w<V, kShift, kPacked, kX>(ring[a], at, ahead);
-        if constexpr (!kAll) load_turn_x<V, kX>(ring[a], at, ahead, p.x_shift);
-        next();
+          for (int a = 0; a < V::kAhead; ++a) {
+            if (turn < end) {
+              add_turn(ring[a], turn * V::kUnits, full);
+              turn += l.k_waves;
+            }
+            refill(ring[a]);
+          }
+        }
       }
-      // places in the ring are fixed, so that nothing waits for a load but its use
-      uint32_t unit = begin;
+      u0 = units ? (units - 1) / stage * stage : 0;        // the last stage is still there
+      flush();
+    } else {
+      if constexpr (kAt == kWhole) {
+        if (units) stage_x<V, kX>(p, x_lds, scales, list, cnt, per, 0, units, stride, s_stride);
+        lds_barrier();
+      }
       for (uint32_t q = 0; q < items; q += V::kAhead) {
 #pragma unroll
         for (int a = 0; a < V::kAhead; ++a) {
           if (q + a < items) {
-            add_turn(ring[a], unit, at.end - unit);
-            unit += V::kUnits;
-            if (unit >= at.end) {
+            add_turn(ring[a], turn * V::kUnits, full);
+            turn += l.k_waves;
+            if (turn >= all_turns) {
               flush();
-              unit = begin;
+              turn = wk;
             }
           }
-          load_turn_w<V, kShift, kPacked, kX>(ring[a], at, ahead);
-          if constexpr (!kAll) load_turn_x<V, kX>(ring[a], at, ahead, p.x_shift);
-          next();
+          refill(ring[a]);
         }
       }
-    } else {
-      for (uint32_t t = 0; t < l.n_loop; ++t) flush();
+      if (!items)
+        for (uint32_t t = 0; t < l.n_loop; ++t) flush();
     }
-    if (kAll || l.k_waves > 1) __syncthreads();          // LDS has been read
+    __syncthreads();                           // LDS has been read
   }
 }
 
-template <int kShift, bool kPacked, int kX, int kR, bool kAll>
-hipError_t launch_variant(const MatvecLaunch& l, uint32_t x_lds, uint32_t groups,
-                          hipStream_t stream) {
+// LDS for the whole of x at most, and for a stage of it.
+constexpr uint32_t kWholeBytes = 72 * 1024, kStageBytes = 48 * 1024;
+
+// LDS that all of x of a pass takes; `steps` scales of a unit.
+uint64_t x_bytes(const MatvecLaunch& l, uint32_t steps) {
+  const uint32_t units = (l.p.k + kUnit - 1) / kUnit;
+  return (uint64_t)l.pass * (units * (kUnit * 2 + steps * 4) + 16);
+}
+
+template <int kShift, bool kPacked, int kX, int kR, int kAt>
+hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
+  using V = Variant<kShift, kPacked, kX, kR, kAt>;
+  const uint32_t units = (l.p.k + kUnit - 1) / kUnit;
+  const uint32_t tiles = (l.p.n + V::kCols - 1) / V::kCols;
+  const uint32_t slots = l.slots ? l.slots : 1;
+  const uint64_t work = (uint64_t)tiles * slots;
+  constexpr uint32_t kCus = 256;
+  // Waves that share a tile: until there are 6 waves for each of 256 compute
+  // units, of four units of k or more (one row of 7168 x 18432: 45 us with two,
+  // 18 with four, 18.5 with eight; one token's 8 experts of 4096 x 7168: 26 with
+  // one, 25 with two, 30 with four). With stages two (8 tokens to 8 of 32 experts
+  // of 4096 x 7168: 80 us, 82 with one, 99 with four) but for the largest calls
+  // (64 tokens to 8 of 256: 520 with one, 634 with two).
+  l.k_waves = kAt == kStages && work < kCus * 64 ? 2 : 1;
+  while (l.k_waves < V::kWaves && l.k_waves * 4 <= units && work * l.k_waves < kCus * 6)
+    l.k_waves *= 2;
+  l.x_lds = kAt == kWithW ? 0 : kAt == kWhole ? (uint32_t)x_bytes(l, V::kSteps) : kStageBytes;
+  if constexpr (kAt == kStages) {
+    // a stage holds one round of the rings at least: 16 rows of one wave's two
+    // units, with 8 scales each, take 17 KB
+    constexpr uint32_t kTurnBytes = V::kUnits * (kUnit * 2 + V::kSteps * 4);
+    static_assert(kR * (V::kAhead * kTurnBytes + 16) <= kStageBytes, "a wave's round");
+    while (l.k_waves > 1 && l.pass * (l.k_waves * V::kAhead * kTurnBytes + 16) > kStageBytes)
+      l.k_waves /= 2;
+  }
+  // Workgroups of 8 waves, two or more to a compute unit; of 16 where LDS has
+  // room for only one (16 tokens to 8 of 32 experts of 7168 x 2048, 66 KB of x:
+  // 60 us, 80 with 8 waves). Where x is whole a workgroup takes two rows of
+  // tiles when there are 48 waves' worth for each compute unit (the same call:
+  // 70 with one; but 32 tokens to 8 of 256 experts of 2048 x 7168, 404 with 5).
+  const uint32_t most = kAt != kWithW && l.x_lds + 8 * V::kLds > 80 * 1024 ? 16 : 8;
+  l.n_waves = l.k_waves < most ? most / l.k_waves : 1;
+  while (l.n_waves > 1 && l.n_waves > tiles) l.n_waves /= 2;
+  l.n_loop = kAt != kStages && work * l.k_waves >= kCus * 48 ? 2 : 1;
+  l.tiles = (tiles + l.n_waves * l.n_loop - 1) / (l.n_waves * l.n_loop);
+  const uint64_t groups = (uint64_t)l.tiles * slots;
   const uint32_t waves = l.n_waves * l.k_waves;
-  launch_kernel(matvec_kernel<kShift, kPacked, kX, kR, kAll>, dim3(groups), dim3(waves * 64),
-                waves * Variant<kShift, kPacked, kX, kR, kAll>::kLds + x_lds, stream, l);
+  if (groups >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
+  static_assert(16 * Variant<0, false, kXStep, 16, kWhole>::kLds + kWholeBytes <= 160 * 1024 &&
+                    8 * Variant<0, false, kXStep, 16, kWithW>::kLds <= 160 * 1024,
+                "LDS");
+  launch_kernel(matvec_kernel<kShift, kPacked, kX, kR, kAt>, dim3((uint32_t)groups),
+                dim3(waves * 64), waves * V::kLds + l.x_lds, stream, l);
   return hipGetLastError();
 }
 
+// Where x is. Whole up to 72 KB (5 rows of 16384 x 5120: 14.7 us, 18.7 with the
+// weights; 16 tokens to 8 of 32 experts of 7168 x 2048: 60, 68 in stages). Past
+// that the rows of an expert come in stages (8 tokens to 8 of 32 experts of
+// 4096 x 7168: 80 us, 109 with the weights), and so do up to four rows without
+// experts; more of those, whose workgroups would each stage all of x for few
+// tiles, with the weights (16 rows of 7168 x 18432: 28 us, 37 in stages).
 template <int kShift, bool kPacked, int kX>
-hipError_t launch_rows(const MatvecLaunch& l, bool all, uint32_t lds, uint32_t groups,
-                       hipStream_t stream) {
+hipError_t launch_rows(const MatvecLaunch& l, hipStream_t stream) {
+  const bool whole = x_bytes(l, Variant<kShift, kPacked, kX, 16, kWhole>::kSteps) <= kWholeBytes;
   if (l.pass <= 4)
-    return all ? launch_variant<kShift, kPacked, kX, 4, true>(l, lds, groups, stream)
-               : launch_variant<kShift, kPacked, kX, 4, false>(l, 0, groups, stream);
-  return all ? launch_variant<kShift, kPacked, kX, 16, true>(l, lds, groups, stream)
-             : launch_variant<kShift, kPacked, kX, 16, false>(l, 0, groups, stream);
+    return whole ? launch_variant<kShift, kPacked, kX, 4, kWhole>(l, stream)
+                 : launch_variant<kShift, kPacked, kX, 4, kStages>(l, stream);
+  return whole     ? launch_variant<kShift, kPacked, kX, 16, kWhole>(l, stream)
+         : l.slots ? launch_variant<kShift, kPacked, kX, 16, kStages>(l, stream)
+                   : launch_variant<kShift, kPacked, kX, 16, kWithW>(l, stream);
 }
 
 template <int kShift, bool kPacked>
-hipError_t launch_x(const MatvecLaunch& l, bool all, uint32_t lds, uint32_t groups,
-                    hipStream_t stream) {
-  return !l.p.x_fmt          ? launch_rows<kShift, kPacked, kXPlain>(l, all, lds, groups, stream)
-         : l.p.x_shift == 2  ? launch_rows<kShift, kPacked, kXBlock>(l, all, lds, groups, stream)
-                             : launch_rows<kShift, kPacked, kXStep>(l, all, lds, groups, stream);
+hipError_t launch_x(const MatvecLaunch& l, hipStream_t stream) {
+  return !l.p.x_fmt         ? launch_rows<kShift, kPacked, kXPlain>(l, stream)
+         : l.p.x_shift == 2 ? launch_rows<kShift, kPacked, kXBlock>(l, stream)
+                            : launch_rows<kShift, kPacked, kXStep>(l, stream);
 }
 
 template <int kShift>
-hipError_t launch_s(const MatvecLaunch& l, bool all, uint32_t lds, uint32_t groups,
-                    hipStream_t stream) {
-  return l.p.packed ? launch_x<kShift, true>(l, all, lds, groups, stream)
-                    : launch_x<kShift, false>(l, all, lds, groups, stream);
+hipError_t launch_s(const MatvecLaunch& l, hipStream_t stream) {
+  return l.p.packed ? launch_x<kShift, true>(l, stream) : launch_x<kShift, false>(l, stream);
 }
 
 int64_t slots_of(int64_t rows, int64_t experts, bool ids) {
@@ -716,45 +809,18 @@ hipError_t launch_matvec(const Matvec& p, hipStream_t stream) {
   l.p = p;
   l.slots = (uint32_t)slots_of(p.rows, p.experts, p.ids != nullptr);
   l.by_row = l.slots == p.rows && (int64_t)p.rows <= p.experts;
-  const uint32_t units = (p.k + kUnit - 1) / kUnit;
-  // rows that one reading of a weight serves
+  // Rows that one reading of a weight serves: all of them up to 16, and of an
+  // expert one where hardly two of the rows share one, four up to a row for each
+  // expert (2 tokens to 8 of 32 experts of 4096 x 7168: 42 us, 45 with 16; 4 to
+  // 8 of 32 of 7168 x 2048 with e4m3: 43 and 48; 32 to 8 of 256: 229 and 207).
   uint32_t rows = p.rows;
-  if (p.ids) {
-    const uint32_t even = (uint32_t)((p.rows + p.experts - 1) / (p.experts ? p.experts : 1));
-    rows = p.rows < 2 * even + 2 ? p.rows : 2 * even + 2;
-    if ((int64_t)p.rows * p.rows <= 4 * p.experts) rows = 1;
-  }
-  l.pass = rows < 16 ? rows : 16;
-  // All of x in LDS where it fits beside the waves' own: 16 tokens to 8 of 32
-  // experts' 7168 x 2048 take 63 us so and 81 otherwise; one row of 18432, 18.9
-  // and 19.8.
-  constexpr uint32_t kXLds = 96 * 1024;
-  const uint32_t row_lds = units * (kUnit * 2 + (!p.x_fmt ? 0 : p.x_shift == 2 ? 8 : 32)) + 16;
-  const bool all = (uint64_t)l.pass * row_lds <= kXLds;
-  const uint32_t lds = all ? l.pass * row_lds : 0;
-  const uint32_t most = all || l.pass <= 4 ? 16 : 8;
-  const uint32_t cols = all || l.pass <= 4 ? 16 : 32;
-  const uint32_t tiles = (p.n + cols - 1) / cols;
-  const uint64_t work = (uint64_t)tiles * (l.slots ? l.slots : 1);
-  // Waves that share a tile: until there are 6 waves for each of 256 compute
-  // units, of four units of k or more (7168 x 18432: 48 us with one, 19 with four,
-  // 24 with 16). Workgroups of 8 waves; tiles one after the other past 24 waves
-  // for each (the 32 experts: 62 us with one, 58 with two, 72 with four).
-  constexpr uint32_t kCus = 256;
-  l.k_waves = 1;
-  while (l.k_waves < most && l.k_waves * 4 <= units && work * l.k_waves < kCus * 6)
-    l.k_waves *= 2;
-  l.n_waves = l.k_waves < 8 ? 8 / l.k_waves : 1;
-  while (l.n_waves > 1 && l.n_waves > tiles) l.n_waves /= 2;
-  const uint64_t loops = work * l.k_waves / (kCus * 24);
-  l.n_loop = loops < 1 ? 1 : loops > 8 ? 8 : (uint32_t)loops;
-  l.tiles = (tiles + l.n_waves * l.n_loop - 1) / (l.n_waves * l.n_loop);
-  const uint64_t groups = (uint64_t)l.tiles * (l.slots ? l.slots : 1);
-  if (groups >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
+  if (p.ids)
+    rows = (int64_t)p.rows * p.rows <= 4 * (int64_t)p.experts ? 1 : p.rows <= p.experts ? 4 : 16;
+  l.pass = p.rows < rows ? p.rows : rows < 16 ? rows : 16;
   switch (p.w_shift) {
-    case 0: return launch_s<0>(l, all, lds, (uint32_t)groups, stream);
-    case 1: return launch_s<1>(l, all, lds, (uint32_t)groups, stream);
-    case 2: return launch_s<2>(l, all, lds, (uint32_t)groups, stream);
+    case 0: return launch_s<0>(l, stream);
+    case 1: return launch_s<1>(l, stream);
+    case 2: return launch_s<2>(l, stream);
   }
   return hipErrorInvalidValue;
 }

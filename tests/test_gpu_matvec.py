@@ -100,6 +100,29 @@ def test_experts(tokens, top_k, experts, dtype, out_dtype):
     check(*activations(g, tokens * top_k, k), codes, sf, 32, ids, out_dtype)
 
 
+@pytest.mark.parametrize("x,x_group", [("bf16", 128), ("e4m3", 32), ("e5m2", 128)])
+@pytest.mark.parametrize("group,packed,k", [(32, False, 2816), (32, False, 3200), (32, False, 5248), (64, False, 9856),
+                                            (32, False, 20480), (128, True, 2560), (128, True, 5632), (128, True, 9728)])
+def test_long_rows_of_experts(x, x_group, group, packed, k):
+    """More of x than LDS takes at once: stages, with and without an end of k
+    that is no whole unit."""
+    g = torch.Generator().manual_seed(k)
+    codes, sf = weights(g, (3,), 40, k, group, packed)
+    for tokens, top_k in ((30, 2), (7, 1), (2, 2)):      # passes of 16, of 7, and of 4
+        ids = moe_ref.routing(tokens, top_k, 4, seed=k, repeat=True) - int(tokens > 7)
+        check(*activations(g, tokens, k, x, x_group), codes, sf, group, ids)
+
+
+@pytest.mark.parametrize("x,x_group", [("bf16", 128), ("e4m3", 64), ("e5m2", 128)])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("rows", [3, 4, 5, 11, 16, 21])
+@pytest.mark.parametrize("k", [5248, 9728, 36992])
+def test_long_rows(x, x_group, group, rows, k):
+    g = torch.Generator().manual_seed(k + rows)
+    codes, sf = weights(g, (), 40, k, group, False)
+    check(*activations(g, rows, k, x, x_group), codes, sf, group)
+
+
 def test_ids_far_outside():
     g = torch.Generator().manual_seed(0)
     codes, sf = weights(g, (2,), 16, 128, 64, False)

@@ -30,6 +30,8 @@
 #include "qcast_kernels.h"
 #include "qcast_row.h"
 
+#include <cmath>
+
 namespace qcast {
 namespace {
 
@@ -722,16 +724,25 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
   const uint32_t slots = l.slots ? l.slots : 1;
   const uint64_t work = (uint64_t)tiles * slots;
   constexpr uint32_t kCus = 256;
+  // x and 8 waves take more than half of LDS: a compute unit has one workgroup
+  const uint64_t whole = x_bytes(l, V::kSteps);
+  l.x_lds = kAt == kWithW ? 0 : kAt == kWhole ? (uint32_t)whole : kStageBytes;
+  const bool alone = kAt != kWithW && l.x_lds + 8 * V::kLds > 80 * 1024;
   // Waves that share a tile: until there are 6 waves for each of 256 compute
   // units, of four units of k or more (one row of 7168 x 18432: 45 us with two,
-  // 18 with four, 18.5 with eight; one token's 8 experts of 4096 x 7168: 26 with
-  // one, 25 with two, 30 with four). With stages two (8 tokens to 8 of 32 experts
-  // of 4096 x 7168: 80 us, 82 with one, 99 with four) but for the largest calls
-  // (64 tokens to 8 of 256: 520 with one, 634 with two).
-  l.k_waves = kAt == kStages && work < kCus * 64 ? 2 : 1;
+  // 18 with four, 18.5 with eight). Two at least, in stages (8 tokens to 8 of 32
+  // experts of 4096 x 7168: 80 us, 82 with one, 99 with four) but for the
+  // largest calls (64 tokens to 8 of 256: 520 with one, 634 with two); with up
+  // to four rows of 4096 k or more (32 to 8 of 256 of 2048 x 7168: 210, 224 with
+  // one; but 4 to 8 of 32 of 7168 x 2048, 43 with one and 49 with two); and in a
+  // workgroup alone on its compute unit (16 to 8 of 32 of 7168 x 2048: 53, 56).
+  const bool two = kAt == kStages ? work < kCus * 64
+                   : kAt == kWithW ? false
+                   : kR == 4       ? units >= 16
+                                   : alone && units >= 8;
+  l.k_waves = two ? 2 : 1;
   while (l.k_waves < V::kWaves && l.k_waves * 4 <= units && work * l.k_waves < kCus * 6)
     l.k_waves *= 2;
-  l.x_lds = kAt == kWithW ? 0 : kAt == kWhole ? (uint32_t)x_bytes(l, V::kSteps) : kStageBytes;
   if constexpr (kAt == kStages) {
     // a stage holds one round of the rings at least: 16 rows of one wave's two
     // units, with 8 scales each, take 17 KB
@@ -740,15 +751,31 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
     while (l.k_waves > 1 && l.pass * (l.k_waves * V::kAhead * kTurnBytes + 16) > kStageBytes)
       l.k_waves /= 2;
   }
-  // Workgroups of 8 waves, two or more to a compute unit; of 16 where LDS has
-  // room for only one (16 tokens to 8 of 32 experts of 7168 x 2048, 66 KB of x:
-  // 60 us, 80 with 8 waves). Where x is whole a workgroup takes two rows of
-  // tiles when there are 48 waves' worth for each compute unit (the same call:
-  // 70 with one; but 32 tokens to 8 of 256 experts of 2048 x 7168, 404 with 5).
-  const uint32_t most = kAt != kWithW && l.x_lds + 8 * V::kLds > 80 * 1024 ? 16 : 8;
+  // Workgroups of 8 waves, of 16 where there is room for only one (66 KB of x,
+  // 16 tokens to 8 of 32 experts of 7168 x 2048 again: 72 us with 8), with half
+  // a workgroup for each compute unit at least (16 rows of 7168 x 2048: 7.8 us
+  // with 8 waves, 9.2 with 16).
+  const uint32_t most = alone ? 16 : 8;
   l.n_waves = l.k_waves < most ? most / l.k_waves : 1;
-  while (l.n_waves > 1 && l.n_waves > tiles) l.n_waves /= 2;
-  l.n_loop = kAt != kStages && work * l.k_waves >= kCus * 48 ? 2 : 1;
+  while (l.n_waves > 1 && (l.n_waves > tiles || work < kCus / 2 * l.n_waves)) l.n_waves /= 2;
+  // Tiles that a wave takes one after the other, x staying where it is. Passes of
+  // four: two, more make an expert with many rows a long tail (32 tokens to 8 of
+  // 256 experts: 210 us with two, 259 with four). Passes of 16: what takes the
+  // fewest rounds of all compute units, the staging of x counted as 8 units (16
+  // tokens to 8 of 32: 87 us with one tile, 74 with two, 64 with four, 53 with
+  // seven, which is one round, 60 with eight).
+  l.n_loop = 1;
+  if (kAt == kWhole && work * l.k_waves >= kCus * 16) {
+    l.n_loop = 2;
+    const double places = alone ? kCus : 2 * kCus;
+    const double live = l.slots ? l.p.experts * (1 - std::exp(-(double)l.p.rows / l.p.experts)) : 1;
+    double least = 1e30;
+    for (uint32_t n = 1; kR == 16 && n <= 8; ++n) {
+      const uint32_t groups = (tiles + l.n_waves * n - 1) / (l.n_waves * n);
+      const double cost = std::ceil(groups * live / places) * (n + 8.0 * l.k_waves / units);
+      if (cost < least) least = cost, l.n_loop = n;
+    }
+  }
   l.tiles = (tiles + l.n_waves * l.n_loop - 1) / (l.n_waves * l.n_loop);
   const uint64_t groups = (uint64_t)l.tiles * slots;
   const uint32_t waves = l.n_waves * l.k_waves;

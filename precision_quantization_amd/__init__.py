@@ -20,6 +20,12 @@ and read by the backward pass (``qcast_swiglu_backward_checkpoint``,
 ``qcast_norm_backward_per_token``, ``qcast_recast_per_channel_T``). These calls
 allocate what they return for the stream they run on.
 
+Around the products of a mixture of experts: slots sorted by expert
+(``qcast_expert_sort``, an ``ExpertPlan``), rows brought there and back
+(``qcast_dispatch_codes``, ``qcast_dispatch_per_token``, ``qcast_combine``,
+``qcast_combine_backward_per_token``), and for decoding products of a few rows
+with E2M1 weights (``qcast_matvec_e2m1``).
+
 ``per_token_cast(x, fmt='e4m3', num_per_channels=128) -> (out, out_sf)``
 mirrors the call shown in the quick start of the page
 "DeepSeek开源TileKernels：用Python写的GPU算子逼近硬件性能上限".

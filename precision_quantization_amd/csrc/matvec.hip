@@ -44,11 +44,13 @@ constexpr uint32_t kXRow = kUnit * 2 + 16; // a unit's row of x in LDS: 4 banks 
 
 struct MatvecLaunch {
   Matvec p;
-  uint32_t tiles;        // workgroups along n
+  uint32_t tiles;        // workgroups along n; with several passes a multiple of 8
   uint32_t n_waves;      // column tiles of a workgroup
   uint32_t k_waves;      // waves that share a column tile
   uint32_t n_loop;       // column tiles that a wave takes one after the other
   uint32_t pass;         // rows that are taken at once
+  uint32_t passes;       // workgroups that share the passes of a slot's tiles
+  bool few;              // no more than two column tiles for each compute unit
   uint32_t x_lds;        // bytes of LDS for x
   uint32_t slots;        // 0: no ids
   bool by_row;           // a slot is a row (the first of its expert), else an expert
@@ -390,8 +392,12 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   const uint32_t lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t wn = wave / l.k_waves, wk = wave - wn * l.k_waves;
-  const uint32_t slot = blockIdx.x / l.tiles;
-  const uint32_t tile0 = ((blockIdx.x - slot * l.tiles) * l.n_waves + wn) * l.n_loop;
+  // the passes of the same tiles are 8 workgroups apart: on one XCD, whose L2
+  // they find the weights in
+  const uint32_t slot = blockIdx.x / (l.tiles * l.passes);
+  const uint32_t b = blockIdx.x - slot * (l.tiles * l.passes);
+  const uint32_t b8 = b / 8, pass0 = b8 % l.passes;
+  const uint32_t tile0 = ((b8 / l.passes * 8 + b % 8) * l.n_waves + wn) * l.n_loop;
 
   auto id_of = [&](uint32_t r) {
     const int64_t id = p.wide ? static_cast<const int64_t*>(p.ids)[r]
@@ -457,8 +463,8 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   };
   // without its own x the first weights are asked for before it is known whose
   // rows they meet
-  if (!kOwn && items) begin();
-  for (uint32_t first = 0;; first += l.pass) {
+  if (!kOwn && items && pass0 == 0) begin();
+  for (uint32_t first = pass0 * l.pass;; first += l.passes * l.pass) {
     // the rows of this pass: those with the slot's expert, l.pass at a time; lane
     // m holds the m-th
     uint32_t cnt = 0, list = 0;
@@ -707,8 +713,19 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   }
 }
 
-// LDS for the whole of x at most, and for a stage of it.
-constexpr uint32_t kWholeBytes = 72 * 1024, kStageBytes = 48 * 1024;
+constexpr uint32_t kCus = 256;
+
+// LDS for the whole of x at most, and for a stage of it; with few tiles, for
+// either: more waves can share one then (44 rows to 2 of 4 experts of 3697 x
+// 14592: 42 us, 51 with stages of 48 KB).
+constexpr uint32_t kWholeBytes = 72 * 1024, kStageBytes = 48 * 1024, kFewBytes = 112 * 1024;
+
+// Experts that the rows hit, were the choice even and a row of x's all different.
+double live_experts(const Matvec& p) {
+  if (p.experts == 0 || p.x_rows == 0) return 0;
+  const double per = (double)(p.rows / p.x_rows) / p.experts;
+  return p.experts * (1 - std::pow(per < 1 ? 1 - per : 0, (double)p.x_rows));
+}
 
 // LDS that all of x of a pass takes; `steps` scales of a unit.
 uint64_t x_bytes(const MatvecLaunch& l, uint32_t steps) {
@@ -722,11 +739,10 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
   const uint32_t units = (l.p.k + kUnit - 1) / kUnit;
   const uint32_t tiles = (l.p.n + V::kCols - 1) / V::kCols;
   const uint32_t slots = l.slots ? l.slots : 1;
-  const uint64_t work = (uint64_t)tiles * slots;
-  constexpr uint32_t kCus = 256;
+  const uint64_t work = (uint64_t)tiles * slots * l.passes;
   // x and 8 waves take more than half of LDS: a compute unit has one workgroup
   const uint64_t whole = x_bytes(l, V::kSteps);
-  l.x_lds = kAt == kWithW ? 0 : kAt == kWhole ? (uint32_t)whole : kStageBytes;
+  l.x_lds = kAt == kWithW ? 0 : kAt == kWhole ? (uint32_t)whole : l.few ? kFewBytes : kStageBytes;
   const bool alone = kAt != kWithW && l.x_lds + 8 * V::kLds > 80 * 1024;
   // Waves that share a tile: until there are 6 waves for each of 256 compute
   // units, of four units of k or more (one row of 7168 x 18432: 45 us with two,
@@ -748,39 +764,41 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
     // units, with 8 scales each, take 17 KB
     constexpr uint32_t kTurnBytes = V::kUnits * (kUnit * 2 + V::kSteps * 4);
     static_assert(kR * (V::kAhead * kTurnBytes + 16) <= kStageBytes, "a wave's round");
-    while (l.k_waves > 1 && l.pass * (l.k_waves * V::kAhead * kTurnBytes + 16) > kStageBytes)
+    while (l.k_waves > 1 && l.pass * (l.k_waves * V::kAhead * kTurnBytes + 16) > l.x_lds)
       l.k_waves /= 2;
   }
-  // Workgroups of 8 waves, of 16 where there is room for only one (66 KB of x,
-  // 16 tokens to 8 of 32 experts of 7168 x 2048 again: 72 us with 8), with half
-  // a workgroup for each compute unit at least (16 rows of 7168 x 2048: 7.8 us
-  // with 8 waves, 9.2 with 16).
-  const uint32_t most = alone ? 16 : 8;
-  l.n_waves = l.k_waves < most ? most / l.k_waves : 1;
-  while (l.n_waves > 1 && (l.n_waves > tiles || work < kCus / 2 * l.n_waves)) l.n_waves /= 2;
-  // Tiles that a wave takes one after the other, x staying where it is. Passes of
-  // four: two, more make an expert with many rows a long tail (32 tokens to 8 of
-  // 256 experts: 210 us with two, 259 with four). Passes of 16: what takes the
-  // fewest rounds of all compute units, the staging of x counted as 8 units (16
-  // tokens to 8 of 32: 87 us with one tile, 74 with two, 64 with four, 53 with
-  // seven, which is one round, 60 with eight).
-  l.n_loop = 1;
-  if (kAt == kWhole && work * l.k_waves >= kCus * 16) {
-    l.n_loop = 2;
-    const double places = alone ? kCus : 2 * kCus;
-    const double live = l.slots ? l.p.experts * (1 - std::exp(-(double)l.p.rows / l.p.experts)) : 1;
-    double least = 1e30;
-    for (uint32_t n = 1; kR == 16 && n <= 8; ++n) {
-      const uint32_t groups = (tiles + l.n_waves * n - 1) / (l.n_waves * n);
-      const double cost = std::ceil(groups * live / places) * (n + 8.0 * l.k_waves / units);
-      if (cost < least) least = cost, l.n_loop = n;
+  // Workgroups of up to 8 waves (16 if alone), and how many column tiles a wave
+  // takes one after the other with x where it is: the least time of the compute
+  // unit with the most workgroups, in times of a unit of k of a tile (0.1 us).
+  // Their work adds up; starts (5 us: ids, x, the first weights) are waited for
+  // once for all that are there together. 16 tokens to 8 of 32 experts of 7168 x
+  // 2048: 87 us with one tile, 74 with two, 64 with four, 53 with seven, 60 with
+  // eight; a token's 4 of 9216 x 7168: 39 with 2 x 4 waves and two tiles, 30 with
+  // 2 x 2 and one. With passes of four two tiles at most: more make an expert
+  // with many rows a long tail (32 tokens to 8 of 256: 210 with two, 259 with four).
+  uint32_t most = (alone ? 16 : kAt == kWithW ? 4 : 8) / l.k_waves;
+  while (most > 1 && most > tiles) most /= 2;
+  if (most == 0) most = 1;
+  const uint32_t loops = kAt != kWhole ? 1 : kR == 4 ? 2 : 8;
+  const double live = l.slots ? live_experts(l.p) : l.passes;
+  constexpr double kStart = 53;
+  double least = 1e300;
+  for (uint32_t n = most; n == most || (n > 0 && n * l.k_waves >= 4); n /= 2) {
+    const uint32_t waves = n * l.k_waves, room = 160 * 1024 / (l.x_lds + waves * V::kLds);
+    const uint32_t together = waves >= 16 || room < 2 ? 1 : room < 16 / waves ? room : 16 / waves;
+    for (uint32_t loop = 1; loop <= loops; ++loop) {
+      const double groups = (double)((tiles + n * loop - 1) / (n * loop)) * live;
+      const double each = std::ceil(groups / kCus);
+      const double cost = each * n * loop * units * V::kTiles + std::ceil(each / together) * kStart;
+      if (cost < least) least = cost, l.n_waves = n, l.n_loop = loop;
     }
   }
   l.tiles = (tiles + l.n_waves * l.n_loop - 1) / (l.n_waves * l.n_loop);
-  const uint64_t groups = (uint64_t)l.tiles * slots;
+  if (l.passes > 1) l.tiles = (l.tiles + 7) / 8 * 8;
+  const uint64_t groups = (uint64_t)l.tiles * slots * l.passes;
   const uint32_t waves = l.n_waves * l.k_waves;
   if (groups >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
-  static_assert(16 * Variant<0, false, kXStep, 16, kWhole>::kLds + kWholeBytes <= 160 * 1024 &&
+  static_assert(16 * Variant<0, false, kXStep, 16, kWhole>::kLds + kFewBytes <= 160 * 1024 &&
                     8 * Variant<0, false, kXStep, 16, kWithW>::kLds <= 160 * 1024,
                 "LDS");
   launch_kernel(matvec_kernel<kShift, kPacked, kX, kR, kAt>, dim3((uint32_t)groups),
@@ -796,7 +814,8 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
 // tiles, with the weights (16 rows of 7168 x 18432: 28 us, 37 in stages).
 template <int kShift, bool kPacked, int kX>
 hipError_t launch_rows(const MatvecLaunch& l, hipStream_t stream) {
-  const bool whole = x_bytes(l, Variant<kShift, kPacked, kX, 16, kWhole>::kSteps) <= kWholeBytes;
+  const bool whole = x_bytes(l, Variant<kShift, kPacked, kX, 16, kWhole>::kSteps) <=
+                     (l.few ? kFewBytes : kWholeBytes);
   if (l.pass <= 4)
     return whole ? launch_variant<kShift, kPacked, kX, 4, kWhole>(l, stream)
                  : launch_variant<kShift, kPacked, kX, 4, kStages>(l, stream);
@@ -836,14 +855,24 @@ hipError_t launch_matvec(const Matvec& p, hipStream_t stream) {
   l.p = p;
   l.slots = (uint32_t)slots_of(p.rows, p.experts, p.ids != nullptr);
   l.by_row = l.slots == p.rows && (int64_t)p.rows <= p.experts;
-  // Rows that one reading of a weight serves: all of them up to 16, and of an
-  // expert one where hardly two of the rows share one, four up to a row for each
-  // expert (2 tokens to 8 of 32 experts of 4096 x 7168: 42 us, 45 with 16; 4 to
-  // 8 of 32 of 7168 x 2048 with e4m3: 43 and 48; 32 to 8 of 256: 229 and 207).
+  // Rows that one reading of a weight serves: all of them up to 16; of an expert
+  // one with one row of x (a token's experts are different ones), four up to a row
+  // for each expert (8 rows to 32 experts of 7168 x 2048: 17 us, 28 with passes of
+  // one; 2 tokens to 8 of 32 of 4096 x 7168: 42 us, 45 with 16; 4 to 8 of 32 of
+  // 7168 x 2048 with e4m3: 43 and 48; 32 to 8 of 256: 210 and 207).
   uint32_t rows = p.rows;
-  if (p.ids)
-    rows = (int64_t)p.rows * p.rows <= 4 * (int64_t)p.experts ? 1 : p.rows <= p.experts ? 4 : 16;
+  if (p.ids) rows = p.x_rows == 1 ? 1 : p.rows <= p.experts ? 4 : 16;
   l.pass = p.rows < rows ? p.rows : rows < 16 ? rows : 16;
+  // Without experts up to 8 passes at the same time (64 rows of 7168 x 7168: 47 us
+  // one after the other, 33; 50 rows of 120 x 5888: 35 and 11). How many an
+  // expert has is not known here, and workgroups that find no rows cost more than
+  // they save (32 tokens to 2 of 8 experts of 14336 x 4096: 68 us, 73 with three).
+  const uint32_t passes = p.ids ? 1 : (p.rows + l.pass - 1) / l.pass;
+  l.passes = passes < 8 ? passes : 8;
+  const uint64_t tiles = ((uint64_t)p.n + 15) / 16 * (l.slots ? l.slots : 1);
+  if ((tiles + 8 * (uint64_t)l.slots + 8) * l.passes >= uint64_t(1) << 31) l.passes = 1;
+  const double here = p.ids ? (p.n + 15) / 16 * live_experts(p) : (double)tiles * l.passes;
+  l.few = here <= 2 * kCus;
   switch (p.w_shift) {
     case 0: return launch_s<0>(l, stream);
     case 1: return launch_s<1>(l, stream);

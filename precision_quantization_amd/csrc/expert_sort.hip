@@ -39,10 +39,11 @@ __device__ __forceinline__ uint64_t same_expert(uint32_t e, uint32_t experts) {
   return same;
 }
 
-// The slots of a wave: [begin, end) of its workgroup's part.
-__device__ __forceinline__ void wave_slots(const ExpertSort& p, uint32_t& begin, uint32_t& end) {
+// The slots of a wave: [begin, end) of the part.
+__device__ __forceinline__ void wave_slots(const ExpertSort& p, uint32_t part, uint32_t& begin,
+                                           uint32_t& end) {
   const uint32_t wave = threadIdx.x >> 6;
-  const uint32_t p0 = blockIdx.x * p.part;
+  const uint32_t p0 = part * p.part;
   const uint32_t p1 = p.slots - p0 < p.part ? p.slots : p0 + p.part;
   const uint32_t per = ((p1 - p0 + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   begin = p1 - p0 < wave * per ? p1 : p0 + wave * per;
@@ -79,7 +80,7 @@ template <uint32_t kExperts>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(ExpertSort p) {
   __shared__ uint32_t counts[kExperts];
   uint32_t begin, end;
-  wave_slots(p, begin, end);
+  wave_slots(p, blockIdx.x, begin, end);
   Slots slots;
   slots.load(p, begin, end);
   for (uint32_t i = threadIdx.x; i < kExperts; i += kSortThreads) counts[i] = 0;
@@ -109,7 +110,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(ExpertSort p) 
   const uint32_t e = threadIdx.x % kExperts, q = threadIdx.x / kExperts;
   const bool mine = e < p.experts;
   uint32_t begin = 0, end = 0;
-  if (p.slots) wave_slots(p, begin, end);
+  // with one part every workgroup counts it, the first has its slots, and all
+  // share the rows without one
+  const uint32_t part = p.ws ? blockIdx.x : 0;
+  if (p.slots) wave_slots(p, part, begin, end);
   Slots slots;
   slots.load(p, begin, end);
   // thread (e, q): the slots of expert e in a kQ-th of the parts
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(ExpertSort p) 
     }
   }
   __syncthreads();
-  slots.each(p, begin, end, [&](uint32_t slot, uint32_t x) {
+  if (part == blockIdx.x) slots.each(p, begin, end, [&](uint32_t slot, uint32_t x) {
     const uint64_t same = same_expert(x, p.experts);
     const uint64_t lower = same & ((1ull << lane) - 1);
     if (x < p.experts) {
@@ -216,7 +220,11 @@ hipError_t launch(const ExpertSort& p, uint32_t parts, hipStream_t stream) {
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
-  launch_kernel(sort_place_kernel<kExperts>, dim3(parts), dim3(kSortThreads), 0, stream, p);
+  // rows without a slot: a workgroup for 4096 rows, up to 16 (512 x 8 slots of 256
+  // experts in runs of 128, 36608 rows: 11.7 us with one workgroup, 8.7 with nine)
+  const uint32_t fill = p.rows / 4096 < 16 ? p.rows / 4096 + 1 : 16;
+  launch_kernel(sort_place_kernel<kExperts>, dim3(parts > 1 ? parts : fill), dim3(kSortThreads),
+                0, stream, p);
   return hipGetLastError();
 }
 

@@ -12,50 +12,61 @@ namespace {
 
 constexpr uint32_t kWaves = kThreads / 64;
 
-// A wave sums 512 columns of one token, eight rows in flight. A row is a buffer
-// of its own (of no bytes for a slot without one: its loads give zeros without
-// reading anything, and its weight is taken as 0).
+// A wave sums 512 columns of kTokens tokens, eight rows in flight. A row is a
+// buffer of its own (of no bytes for a slot without one: its loads give zeros
+// without reading anything, and its weight is taken as 0).
+template <int kTokens>
 __global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t segs) {
+  constexpr uint32_t kSlots = kBatch / kTokens;        // of a token, at once
   const uint32_t lane = threadIdx.x & 63;
   const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / segs));
+  const uint32_t t0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / segs)) * kTokens;
   const uint32_t seg = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % segs));
-  if (t >= p.tokens) return;
+  if (t0 >= p.tokens) return;
   const uint32_t c = seg * 64 + lane, bytes = p.chunks * 16;
-  const uint64_t slot = (uint64_t)t * p.top_k;
-  float acc[8] = {};
+  float acc[kTokens][8] = {};
   if (p.base)
-    unpack8(buffer_load16<0>(row_buffer(p.base, (uint64_t)t * bytes, bytes), c * 16), acc);
-  for (uint32_t k = 0; k < p.top_k; k += kBatch) {
+#pragma unroll
+    for (uint32_t i = 0; i < kTokens; ++i) {
+      const bool in = t0 + i < p.tokens;
+      unpack8(buffer_load16<0>(row_buffer(p.base, in ? (uint64_t)(t0 + i) * bytes : 0,
+                                          in ? bytes : 0), c * 16), acc[i]);
+    }
+  for (uint32_t k = 0; k < p.top_k; k += kSlots) {
     uint32_t r[kBatch];
     float w[kBatch];
-    if (p.dest) {
-      slot_rows(p.dest + slot, k, p.top_k, r);
-    } else {
+    // a slot past the token's last or of no token: another's number, and no row
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) r[j] = k + j < p.top_k ? (uint32_t)slot + k + j : kNoRow;
+    for (uint32_t j = 0; j < kBatch; ++j) {
+      const uint32_t t = t0 + j / kSlots < p.tokens ? t0 + j / kSlots : t0;
+      const uint32_t at = k + j % kSlots < p.top_k ? k + j % kSlots : p.top_k - 1;
+      const uint64_t slot = (uint64_t)t * p.top_k + at;
+      r[j] = p.dest ? (uint32_t)p.dest[slot] : (uint32_t)slot;
+      w[j] = p.weight ? p.weight[slot] : 1.0f;
     }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      w[j] = p.weight ? p.weight[slot + (k + j < p.top_k ? k + j : p.top_k - 1)] : 1.0f;
     u32x4 v[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const bool in = r[j] < p.rows;
+    for (uint32_t j = 0; j < kBatch; ++j) {
+      const bool in = r[j] < p.rows && k + j % kSlots < p.top_k && t0 + j / kSlots < p.tokens;
       v[j] = buffer_load16(row_buffer(p.y, in ? (uint64_t)r[j] * bytes : 0, in ? bytes : 0),
                            c * 16);
       w[j] = in ? w[j] : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (uint32_t j = 0; j < kBatch; ++j) {
       float f[8];
       unpack8(v[j], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+      for (int i = 0; i < 8; ++i)
+        acc[j / kSlots][i] = __builtin_fmaf(w[j], f[i], acc[j / kSlots][i]);
     }
   }
   if (c < p.chunks)
-    store_stream(reinterpret_cast<u32x4*>(p.out) + (uint64_t)t * p.chunks + c, pack8_bf16(acc));
+#pragma unroll
+    for (uint32_t i = 0; i < kTokens; ++i)
+      if (t0 + i < p.tokens)
+        store_stream(reinterpret_cast<u32x4*>(p.out) + (uint64_t)(t0 + i) * p.chunks + c,
+                     pack8_bf16(acc[i]));
 }
 
 // A wave takes one slot over all columns, 512 at a time, with the next 512 asked
@@ -131,10 +142,17 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast
 
 hipError_t launch_combine(const Combine& p, hipStream_t stream) {
   const uint32_t segs = (p.chunks + 63) / 64;
-  const uint64_t groups = ((uint64_t)p.tokens * segs + kWaves - 1) / kWaves;
+  // Four tokens of one or two slots where there is more than the card holds at
+  // once, 8192 waves, twice over (16384 x 1 x 2048: 40 us with one token a wave, 32
+  // with four; 8399 x 2 x 1408, a quarter of the slots with rows: 17.6 and 13.1;
+  // two tokens of four slots, 8192 x 4 x 2048: 33.4 and 33.8).
+  const bool four = p.top_k <= 2 && (uint64_t)p.tokens * segs >= 2 * 8192;
+  const uint32_t tokens = four ? 4 : 1;
+  const uint64_t items = ((uint64_t)p.tokens + tokens - 1) / tokens * segs;
+  const uint64_t groups = (items + kWaves - 1) / kWaves;
   if (groups >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
   if (groups == 0) return hipSuccess;
-  launch_kernel(combine_kernel, dim3((uint32_t)groups), dim3(kThreads), 0, stream, p, segs);
+  launch_kernel(four ? combine_kernel<4> : combine_kernel<1>, dim3((uint32_t)groups), dim3(kThreads), 0, stream, p, segs);
   return hipGetLastError();
 }
 

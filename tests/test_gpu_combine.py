@@ -49,6 +49,29 @@ def test_combine(tokens, top_k, experts, align, cols, weighted, based):
     near(got, want, mag, top_k, "combine")
 
 
+@pytest.mark.parametrize("top_k,weighted,based", [(1, True, False), (2, True, True), (2, False, False)])
+def test_many_tokens_of_few_slots(top_k, weighted, based):
+    """A count of tokens that no group of them divides, some without a row."""
+    tokens, experts, cols = 8203, 8, 1032
+    plan, dest, source, *_ = plan_of(tokens, top_k, experts, 16, total=experts + 3, first=1)
+    g = torch.Generator().manual_seed(top_k)
+    y = torch.randn(source.size, cols, generator=g).to(torch.bfloat16)
+    y[torch.from_numpy(source < 0)] = float("nan")
+    w = torch.randn(tokens, top_k, generator=g) if weighted else None
+    base = torch.randn(tokens, cols, generator=g).to(torch.bfloat16) if based else None
+    out = filled((tokens, cols), torch.bfloat16)
+    got = pq.qcast_combine(y.to(DEV), plan.dest, None if w is None else w.to(DEV),
+                           None if base is None else base.to(DEV), out=out)
+    want, mag = moe_ref.combine(y, dest, w, base)
+    near(got, want, mag, top_k, "combine")
+    # rows that were never sorted
+    flat = torch.randn(tokens * top_k, cols, generator=g).to(torch.bfloat16)
+    got = pq.qcast_combine(flat.to(DEV), None, None if w is None else w.to(DEV),
+                           None if base is None else base.to(DEV), top_k=top_k)
+    want, mag = moe_ref.combine(flat, np.arange(tokens * top_k).reshape(tokens, top_k), w, base)
+    near(got, want, mag, top_k, "combine of rows as they are")
+
+
 def test_tokens_without_rows_and_rows_of_several_slots():
     dest = np.array([[-1, -1, 9], [4, 4, 4], [8, 0, -5], [2 ** 31 - 1, -2 ** 31, 8]], np.int32)
     g = torch.Generator().manual_seed(3)

@@ -464,14 +464,17 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   // without its own x the first weights are asked for before it is known whose
   // rows they meet
   if (!kOwn && items && pass0 == 0) begin();
+  uint32_t from = 0, before = 0;               // ids that are read, their rows of this expert
   for (uint32_t first = pass0 * l.pass;; first += l.passes * l.pass) {
     // the rows of this pass: those with the slot's expert, l.pass at a time; lane
-    // m holds the m-th
+    // m holds the m-th. The next pass goes on with the last 64 ids of this one.
     uint32_t cnt = 0, list = 0;
     if (l.slots) {
-      uint32_t seen = 0;
+      uint32_t seen = before;
       bool leads = true;
-      for (uint32_t r0 = 0; r0 < p.rows; r0 += 64) {
+      for (uint32_t r0 = from; r0 < p.rows && seen < first + l.pass; r0 += 64) {
+        from = r0;
+        before = seen;
         const uint32_t r = r0 + lane;
         bool same = false;
         if (r < p.rows) same = none && l.by_row ? r == slot : id_of(r) == expert;
@@ -861,7 +864,7 @@ hipError_t launch_matvec(const Matvec& p, hipStream_t stream) {
   // one; 2 tokens to 8 of 32 of 4096 x 7168: 42 us, 45 with 16; 4 to 8 of 32 of
   // 7168 x 2048 with e4m3: 43 and 48; 32 to 8 of 256: 210 and 207).
   uint32_t rows = p.rows;
-  if (p.ids) rows = p.x_rows == 1 ? 1 : p.rows <= p.experts ? 4 : 16;
+  if (p.ids) rows = p.rows > p.experts ? 16 : p.x_rows == 1 ? 1 : 4;
   l.pass = p.rows < rows ? p.rows : rows < 16 ? rows : 16;
   // Without experts up to 8 passes at the same time (64 rows of 7168 x 7168: 47 us
   // one after the other, 33; 50 rows of 120 x 5888: 35 and 11). How many an

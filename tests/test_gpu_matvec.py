@@ -123,6 +123,18 @@ def test_long_rows(x, x_group, group, rows, k):
     check(*activations(g, rows, k, x, x_group), codes, sf, group)
 
 
+@pytest.mark.parametrize("tokens,top_k,experts", [(5000, 1, 2), (1500, 8, 3), (257, 4, 1024), (65, 1, 1)])
+def test_many_rows_of_experts(tokens, top_k, experts):
+    """Many passes of an expert, whose rows are thousands of ids apart or next
+    to one another."""
+    g = torch.Generator().manual_seed(tokens)
+    codes, sf = weights(g, (experts,), 20, 64, 32, False)
+    ids = moe_ref.routing(tokens, top_k, experts, seed=tokens, repeat=True)
+    check(*activations(g, tokens, 64), codes, sf, 32, ids)
+    ids = torch.sort(ids.reshape(-1)).values.reshape(tokens, top_k)
+    check(*activations(g, tokens * top_k, 64), codes, sf, 32, ids)
+
+
 def test_ids_far_outside():
     g = torch.Generator().manual_seed(0)
     codes, sf = weights(g, (2,), 16, 128, 64, False)

@@ -431,7 +431,7 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   const uint32_t turns = wk < all_turns ? (all_turns - wk - 1) / l.k_waves + 1 : 0;
   const uint32_t items = turns * l.n_loop;
   const bool ends = !none && p.k % kUnit != 0 && wk == l.k_waves - 1;
-  const uint32_t per = l.slots ? p.rows / p.x_rows : 1;
+  const uint32_t per = p.rows / p.x_rows;     // rows of a row of x, with ids or without
   uint8_t* const mine = lds + wave * V::kLds;
   uint8_t* const x_lds = lds + l.n_waves * l.k_waves * V::kLds;
   const uint8_t* const sa = mine + n * V::kSfRow;

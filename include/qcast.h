@@ -740,7 +740,8 @@ QCAST_API int qcast_combine_backward_per_token(
  *   w        [experts, n, k/2] codes as qcast_e2m1 writes them for the weights'
  *            rows; w_sf [experts, n, k/w_group] fp32, or with
  *            QCAST_SF_PACKED_UE8M0 in w_sf_flags its packed words [experts, n,
- *            k/w_group/4] ((k/w_group) % 4 == 0). Other bits of w_sf_flags:
+ *            k/w_group/4] ((k/w_group) % 4 == 0): byte b is 2^(b - 127), down
+ *            to 2^-127 for 0, and NaN for 255. Other bits of w_sf_flags:
  *            QCAST_SF_ROUND_POW2 changes nothing, QCAST_SF_COL_MAJOR is
  *            QCAST_ERR_FORMAT.
  *   ids      [rows] int32 (id_bytes 4) or int64 (8): each row's expert; a row
@@ -752,6 +753,9 @@ QCAST_API int qcast_combine_backward_per_token(
  *   w_group, x_group  32, 64 or 128; k % w_group == 0 (k % x_group == 0).
  *   out      [rows, n] bf16 (QCAST_OUT_BF16) or fp32 (QCAST_OUT_F32). With
  *            k == 0 it is zeros.
+ *   Products of w's codes with x (bf16, or its codes) are summed over up to 128 k
+ *   ahead of the scales, w_sf is applied ahead of x_sf or as w_sf * x_sf: these
+ *   sums and products have to stay within fp32's range.
  *   Made for up to some 16 rows an expert: more are taken 16 at a time, each
  *   time reading the weights again.
  *   Limits: rows, n, experts < 2^31, k < 2^24, rows * n < 2^40, and fewer than 2^31

@@ -297,6 +297,14 @@ __device__ __forceinline__ void load_own_tail(typename V::Turn& t, const OwnRows
   }
 }
 
+// The fp32 of a UE8M0 byte: 2^(b - 127), subnormal for 0, and NaN for 255. The
+// conversions' scale is the exponent field of an fp32, read so: one times it.
+__device__ __forceinline__ uint32_t e8m0(uint32_t b) {
+  constexpr int kOne = 0x38;             // E4M3
+  return __float_as_uint(
+      __builtin_amdgcn_cvt_scalef32_f32_fp8(kOne, __uint_as_float(b << 23), 0));
+}
+
 // The turn's scales of w to the wave's LDS, as fp32.
 template <typename V, bool kPacked>
 __device__ __forceinline__ void store_scales(const typename V::Turn& t, uint8_t* mine) {
@@ -309,7 +317,7 @@ __device__ __forceinline__ void store_scales(const typename V::Turn& t, uint8_t*
     uint32_t f[V::kPer];
 #pragma unroll
     for (int g = 0; g < V::kPer; ++g)
-      f[g] = kPacked ? (t.sf[t2][0] >> (8 * g) & 0xffu) << 23 : t.sf[t2][g];
+      f[g] = kPacked ? e8m0(t.sf[t2][0] >> (8 * g) & 0xffu) : t.sf[t2][g];
     if constexpr (V::kPer == 4) *reinterpret_cast<u32x4*>(to) = u32x4{f[0], f[1], f[2], f[3]};
     else if constexpr (V::kPer == 2) *reinterpret_cast<u32x2*>(to) = u32x2{f[0], f[1]};
     else *reinterpret_cast<uint32_t*>(to) = f[0];

@@ -16,10 +16,11 @@ constexpr uint32_t kWaves = kThreads / 64;
 // buffer of its own (of no bytes for a slot without one: its loads give zeros
 // without reading anything, and its weight is taken as 0).
 template <int kTokens>
-__global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t segs) {
+__global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t segs,
+                                                           uint32_t first) {
   constexpr uint32_t kSlots = kBatch / kTokens;        // of a token, at once
   const uint32_t lane = threadIdx.x & 63;
-  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint64_t item = (uint64_t)(blockIdx.x + first) * kWaves + (threadIdx.x >> 6);
   const uint32_t t0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / segs)) * kTokens;
   const uint32_t seg = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % segs));
   if (t0 >= p.tokens) return;
@@ -77,11 +78,12 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t s
 // (151); 257 x 6 x 2048: 6.0, 6.4, 8.7 and 9.2.
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast p,
-                                                                    uint32_t groups) {
-  const uint32_t lane = threadIdx.x & 63;
-  if (blockIdx.x >= groups) {
+                                                                    uint32_t groups,
+                                                                    uint32_t first) {
+  const uint32_t lane = threadIdx.x & 63, group = blockIdx.x + first;
+  if (group >= groups) {
     uint32_t r0, r1;
-    pad_range(p.runs, blockIdx.x - groups, r0, r1);
+    pad_range(p.runs, group - groups, r0, r1);
     const float zero[8] = {};
     for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads) {
       const ChunkScale s = chunk_scale<kFmt>(p.cast, c, zero);
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast
     return;
   }
   const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane(
-      (int)(blockIdx.x * kWaves + (threadIdx.x >> 6)));
+      (int)(group * kWaves + (threadIdx.x >> 6)));
   if (slot >= p.runs.tokens * p.runs.top_k) return;
   const uint32_t t = slot / p.runs.top_k, bytes = p.chunks * 16;
   const uint32_t r = (uint32_t)p.runs.dest[slot];
@@ -151,22 +153,19 @@ hipError_t launch_combine(const Combine& p, hipStream_t stream) {
   const uint64_t items = ((uint64_t)p.tokens + tokens - 1) / tokens * segs;
   const uint64_t groups = (items + kWaves - 1) / kWaves;
   if (groups >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
-  if (groups == 0) return hipSuccess;
-  launch_kernel(four ? combine_kernel<4> : combine_kernel<1>, dim3((uint32_t)groups), dim3(kThreads), 0, stream, p, segs);
-  return hipGetLastError();
+  return launch_groups(four ? combine_kernel<4> : combine_kernel<1>, groups, kThreads, stream, p,
+                       segs);
 }
 
 hipError_t launch_combine_backward(const DispatchCast& p, hipStream_t stream) {
   const uint64_t groups = ((uint64_t)p.runs.tokens * p.runs.top_k + kWaves - 1) / kWaves;
   const uint64_t all = groups + (p.cast.q || p.dy ? pad_groups(p.runs) : 0);
   if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
-  if (all == 0) return hipSuccess;
   auto kernel = p.cast.fmt == kE4M3   ? combine_backward_kernel<kE4M3>
                 : p.cast.fmt == kE5M2 ? combine_backward_kernel<kE5M2>
                 : p.cast.fmt == kE2M1 ? combine_backward_kernel<kE2M1>
                                       : combine_backward_kernel<kE5M6>;
-  launch_kernel(kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, (uint32_t)groups);
-  return hipGetLastError();
+  return launch_groups(kernel, all, kThreads, stream, p, (uint32_t)groups);
 }
 
 }  // namespace qcast

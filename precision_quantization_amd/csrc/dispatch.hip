@@ -21,12 +21,13 @@ __device__ __forceinline__ uint32_t scale_index(uint32_t row, uint32_t w, uint32
 
 // Pieces of a token: kSeg of 64 chunks each, then one for its scales.
 __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes p, uint32_t pieces,
-                                                                  uint32_t groups) {
-  const uint32_t lane = threadIdx.x & 63;
+                                                                  uint32_t groups,
+                                                                  uint32_t first) {
+  const uint32_t lane = threadIdx.x & 63, group = blockIdx.x + first;
   const uint32_t segs = (p.chunks + 63) / 64;
-  if (blockIdx.x >= groups) {
+  if (group >= groups) {
     uint32_t r0, r1;
-    pad_range(p.runs, blockIdx.x - groups, r0, r1);
+    pad_range(p.runs, group - groups, r0, r1);
     for (uint32_t r = r0; r < r1; ++r) {
       for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads)
         store_stream(p.out + (uint64_t)r * p.chunks + c, u32x4{0, 0, 0, 0});
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes 
     }
     return;
   }
-  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint64_t item = (uint64_t)group * kWaves + (threadIdx.x >> 6);
   const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / pieces));
   const uint32_t piece = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % pieces));
   if (t >= p.runs.tokens) return;
@@ -69,11 +70,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes 
 // Without weights a row is cast once, whatever the number of its places.
 template <int kFmt, bool kWeighted>
 __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p, uint32_t segs,
-                                                                 uint32_t groups) {
-  const uint32_t lane = threadIdx.x & 63;
-  if (blockIdx.x >= groups) {
+                                                                 uint32_t groups, uint32_t first) {
+  const uint32_t lane = threadIdx.x & 63, group = blockIdx.x + first;
+  if (group >= groups) {
     uint32_t r0, r1;
-    pad_range(p.runs, blockIdx.x - groups, r0, r1);
+    pad_range(p.runs, group - groups, r0, r1);
     const float zero[8] = {};
     for (uint32_t c = threadIdx.x; c < p.chunks; c += kThreads) {
       const ChunkScale s = chunk_scale<kFmt>(p.cast, c, zero);
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p,
     }
     return;
   }
-  const uint64_t item = (uint64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint64_t item = (uint64_t)group * kWaves + (threadIdx.x >> 6);
   const uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item / segs));
   const uint32_t seg = (uint32_t)__builtin_amdgcn_readfirstlane((int)(item % segs));
   const uint32_t c = seg * 64 + lane;
@@ -132,10 +133,8 @@ hipError_t launch_dispatch_codes(const DispatchCodes& p, hipStream_t stream) {
   const uint64_t groups = ((uint64_t)p.runs.tokens * pieces + kWaves - 1) / kWaves;
   const uint64_t all = groups + pad_groups(p.runs);
   if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
-  if (all == 0) return hipSuccess;
-  launch_kernel(dispatch_codes_kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, pieces,
-                (uint32_t)groups);
-  return hipGetLastError();
+  return launch_groups(dispatch_codes_kernel, all, kThreads, stream, p, pieces,
+                       (uint32_t)groups);
 }
 
 hipError_t launch_dispatch_cast(const DispatchCast& p, hipStream_t stream) {
@@ -143,15 +142,12 @@ hipError_t launch_dispatch_cast(const DispatchCast& p, hipStream_t stream) {
   const uint64_t groups = ((uint64_t)p.runs.tokens * segs + kWaves - 1) / kWaves;
   const uint64_t all = groups + pad_groups(p.runs);
   if (all >= (uint64_t(1) << 31)) return hipErrorInvalidValue;
-  if (all == 0) return hipSuccess;
   const bool w = p.weight != nullptr;
   auto kernel = p.cast.fmt == kE4M3   ? cast_kernel<kE4M3>(w)
                 : p.cast.fmt == kE5M2 ? cast_kernel<kE5M2>(w)
                 : p.cast.fmt == kE2M1 ? cast_kernel<kE2M1>(w)
                                       : cast_kernel<kE5M6>(w);
-  launch_kernel(kernel, dim3((uint32_t)all), dim3(kThreads), 0, stream, p, segs,
-                (uint32_t)groups);
-  return hipGetLastError();
+  return launch_groups(kernel, all, kThreads, stream, p, segs, (uint32_t)groups);
 }
 
 }  // namespace qcast

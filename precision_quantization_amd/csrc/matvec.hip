@@ -44,6 +44,7 @@ constexpr uint32_t kXRow = kUnit * 2 + 16; // a unit's row of x in LDS: 4 banks 
 
 struct MatvecLaunch {
   Matvec p;
+  uint32_t first;        // the first workgroup's number
   uint32_t tiles;        // workgroups along n; with several passes a multiple of 8
   uint32_t n_waves;      // column tiles of a workgroup
   uint32_t k_waves;      // waves that share a column tile
@@ -402,8 +403,8 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   const uint32_t wn = wave / l.k_waves, wk = wave - wn * l.k_waves;
   // the passes of the same tiles are 8 workgroups apart: on one XCD, whose L2
   // they find the weights in
-  const uint32_t slot = blockIdx.x / (l.tiles * l.passes);
-  const uint32_t b = blockIdx.x - slot * (l.tiles * l.passes);
+  const uint32_t group = blockIdx.x + l.first, slot = group / (l.tiles * l.passes);
+  const uint32_t b = group - slot * (l.tiles * l.passes);
   const uint32_t b8 = b / 8, pass0 = b8 % l.passes;
   const uint32_t tile0 = ((b8 / l.passes * 8 + b % 8) * l.n_waves + wn) * l.n_loop;
 
@@ -812,9 +813,11 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
   static_assert(16 * Variant<0, false, kXStep, 16, kWhole>::kLds + kFewBytes <= 160 * 1024 &&
                     8 * Variant<0, false, kXStep, 16, kWithW>::kLds <= 160 * 1024,
                 "LDS");
-  launch_kernel(matvec_kernel<kShift, kPacked, kX, kR, kAt>, dim3((uint32_t)groups),
-                dim3(waves * 64), waves * V::kLds + l.x_lds, stream, l);
-  return hipGetLastError();
+  return each_launch(groups, waves * 64, [&](uint32_t first, uint32_t n) {
+    l.first = first;
+    launch_kernel(matvec_kernel<kShift, kPacked, kX, kR, kAt>, dim3(n), dim3(waves * 64),
+                  waves * V::kLds + l.x_lds, stream, l);
+  });
 }
 
 // Where x is. Whole up to 72 KB (5 rows of 16384 x 5120: 14.7 us, 18.7 with the

@@ -29,6 +29,29 @@ inline void launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, uint3
   hipExtLaunchKernelGGL(kernel, grid, block, shmem, stream, t.start, t.stop, 0u, args...);
 }
 
+// A grid has fewer than 2^32 threads: more workgroups than that take several
+// launches, launch(first workgroup's number, workgroups). Whole ones are a
+// multiple of the 8 XCDs long.
+template <typename F>
+inline hipError_t each_launch(uint64_t groups, uint32_t threads, F&& launch) {
+  const uint64_t most = ((uint64_t(1) << 32) / threads - 1) / 8 * 8;
+  for (uint64_t first = 0; first < groups; first += most) {
+    launch((uint32_t)first, (uint32_t)(groups - first < most ? groups - first : most));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+// The same for a kernel whose last argument is the first workgroup's number.
+template <typename... KArgs, typename... Args>
+inline hipError_t launch_groups(void (*kernel)(KArgs...), uint64_t groups, uint32_t threads,
+                                hipStream_t stream, const Args&... args) {
+  return each_launch(groups, threads, [&](uint32_t first, uint32_t n) {
+    launch_kernel(kernel, dim3(n), dim3(threads), 0, stream, args..., first);
+  });
+}
+
 // Whether a shape fits the kernels' 32-bit tile counts and in-tile offsets
 // (checked by the C ABI before any HIP call; the launchers check again).
 bool per_block_fits(int64_t rows, int64_t cols);

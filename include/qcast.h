@@ -674,7 +674,8 @@ QCAST_API int qcast_expert_sort(const void* ids, int id_bytes, int64_t tokens, i
  *            padding rows of each run are written as zeros, scales too. NULL
  *            (both), or align 1: no padding.
  *   Rows of out that are neither are left as they were. rows * sf_words <
- *   2^31 and tokens * sf_words < 2^31.
+ *   2^31 and tokens * sf_words < 2^31 (column-major also < 2^32 with the rows
+ *   rounded up to a multiple of 4).
  */
 QCAST_API int qcast_dispatch_codes(const void* in, int64_t tokens, int64_t row_bytes,
                                    const void* sf_in, int64_t sf_words, int sf_flags_in,

@@ -236,6 +236,14 @@ int check_row_cast(int64_t tokens, int64_t rows, int64_t cols, int fmt, int grou
   return QCAST_OK;
 }
 
+// Scale words of `rows` rows, and their places in the layout of `flags`, which
+// the kernel counts in 32 bits.
+bool words_ok(int64_t rows, int64_t words, int flags) {
+  if (words == 0) return true;
+  if (rows > kInt31 / words) return false;
+  return !(flags & QCAST_SF_COL_MAJOR) || (rows + 3) / 4 * 4 * words < (int64_t(1) << 32);
+}
+
 // Pieces of 512 columns.
 int64_t column_pieces(int64_t cols) { return cols / 512 + 1; }
 
@@ -811,7 +819,7 @@ int qcast_dispatch_codes(const void* in, int64_t tokens, int64_t row_bytes, cons
   if (const int rc = check_runs(tokens, top_k, row_bytes / 1024 + 2, offsets, counts, experts,
                                 align, rows))
     return rc;
-  if (sf_words > 0 && (rows > kInt31 / sf_words || tokens > kInt31 / sf_words))
+  if (!words_ok(rows, sf_words, sf_flags_out) || !words_ok(tokens, sf_words, sf_flags_in))
     return QCAST_ERR_SHAPE;
   if (tokens == 0 || top_k == 0 || rows == 0 || row_bytes == 0) return QCAST_OK;
   if (!in || !out || !dest || (sf_in != nullptr) != (sf_out != nullptr)) return QCAST_ERR_NULL;

@@ -1,0 +1,20 @@
+"""Sizes at the limits of the mixture-of-experts entry points, before any HIP
+call."""
+import pytest
+
+from conftest import gpu_available
+from test_abi_moe import ERR_DEVICE, ERR_SHAPE, codes, lib  # noqa: F401
+
+ROW, COL = 0, 2
+
+
+@pytest.mark.parametrize("rows", ["rows", "tokens"])
+def test_column_major_scales_count_their_padding(lib, rows):  # noqa: F811
+    """One row takes four words of each column: 2^30 columns are past 32 bits."""
+    side, other = dict(rows=("fout", "tokens"), tokens=("fin", "rows"))[rows]
+    for n, words in ((1, 1 << 30), (1, (1 << 31) - 1)):
+        assert codes(lib, **{rows: n, other: 1, "words": words, side: COL}) == ERR_SHAPE, (n, words)
+    if not gpu_available():
+        for n, words in ((1, (1 << 30) - 1), (3, ((1 << 31) - 1) // 3), (5, ((1 << 31) - 1) // 5)):
+            assert codes(lib, **{rows: n, other: 1, "words": words, side: COL}) == ERR_DEVICE, (n, words)
+            assert codes(lib, **{rows: n, other: 1, "words": words, side: ROW}) == ERR_DEVICE, (n, words)

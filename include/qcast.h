@@ -49,7 +49,8 @@
  *    over no rows that a call returns are written as zeros).
  *  - Shapes past the kernels' 32-bit indexing return QCAST_ERR_SHAPE before
  *    any HIP call: rows * cols / group < 2^31 scale groups for the per-token
- *    casts; for the others, the limits stated with each entry point.
+ *    casts (column-major fp32 scales also < 2^32 with the rows rounded up to a
+ *    multiple of 4); for the others, the limits stated with each entry point.
  *  - Calls on one stream are ordered; concurrent calls on different streams
  *    are independent (a count workspace is the caller's, and concurrent
  *    calls need different ones). The one piece of mutable device state the

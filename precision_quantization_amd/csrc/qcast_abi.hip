@@ -114,12 +114,16 @@ bool sf_flags_ok(int flags) {
   return (flags & ~(QCAST_SF_ROUND_POW2 | QCAST_SF_COL_MAJOR | QCAST_SF_PACKED_UE8M0)) == 0;
 }
 
-// Group indices are 32-bit in the scale store; packed words need whole
-// quadruples of groups in every row.
+// Group indices are 32-bit in the scale store, places in a column-major layout
+// (rows up to a multiple of 4) too; packed words need whole quadruples of groups
+// in every row.
 bool sf_shape_ok(int64_t rows, int64_t cols, int group, int flags) {
   if (cols > 0 && rows > ((int64_t(1) << 31) - 1) / (cols / group > 0 ? cols / group : 1))
     return false;
   if ((flags & QCAST_SF_PACKED_UE8M0) && (cols / group) % 4 != 0) return false;
+  // rows * groups < 2^31 here: only a single row's padding, four times it, passes 2^32
+  if ((flags & QCAST_SF_COL_MAJOR) && !(flags & QCAST_SF_PACKED_UE8M0) && rows == 1)
+    return cols / group < (int64_t(1) << 30);
   return true;
 }
 

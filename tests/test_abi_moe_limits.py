@@ -18,3 +18,15 @@ def test_column_major_scales_count_their_padding(lib, rows):  # noqa: F811
         for n, words in ((1, (1 << 30) - 1), (3, ((1 << 31) - 1) // 3), (5, ((1 << 31) - 1) // 5)):
             assert codes(lib, **{rows: n, other: 1, "words": words, side: COL}) == ERR_DEVICE, (n, words)
             assert codes(lib, **{rows: n, other: 1, "words": words, side: ROW}) == ERR_DEVICE, (n, words)
+
+
+def test_column_major_scales_of_one_long_row(lib):  # noqa: F811
+    """The same of the casts: 2^30 groups of a single row."""
+    A, E4M3 = 0x10000, 1
+
+    def cast(cols, group, flags, rows=1):
+        return lib.qcast_per_token_sf(A, rows, cols, E4M3, group, 0.0, flags, A, A, None)
+    assert cast(1 << 36, 64, COL) == cast(1 << 37, 128, COL) == ERR_SHAPE
+    if not gpu_available():
+        assert cast((1 << 36) - 64, 64, COL) == cast(1 << 36, 64, ROW) == cast(1 << 36, 64, COL | 4) == ERR_DEVICE
+        assert cast(128 * ((1 << 31) // 3), 128, COL, rows=3) == ERR_DEVICE

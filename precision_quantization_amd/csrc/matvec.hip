@@ -29,6 +29,7 @@
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
+#include "qcast_stages.h"
 
 #include <cmath>
 
@@ -130,6 +131,7 @@ struct Variant {
   static constexpr int kGroups = kUnits * 8 >> kShift; // of a row of w, in a turn
   static constexpr int kPer = kGroups >= 4 ? kGroups / 4 : 1;   // of them, one lane's
   static constexpr int kSteps = kX == kXPlain ? 0 : kX == kXStep ? 8 : 2;  // scales of a unit of x
+  static constexpr uint32_t kXUnit = kUnit * 2 + kSteps * 4;   // bytes of a unit of a row of x
   static constexpr uint32_t kSfRow = kGroups * 4 + 16; // a row's scales in LDS
   // a wave's LDS: its scales of w, its x, and its sums of two tiles
   static constexpr uint32_t kXAt = 16 * kTiles * kSfRow;
@@ -524,12 +526,9 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
     // x in LDS: all of it, or stages of as many units as fit, in whole rounds of
     // the waves' rings (the launch sees to it that one fits)
     const uint32_t units = none ? 0 : (p.k + kUnit - 1) / kUnit;
-    const uint32_t round = l.k_waves * V::kUnits * V::kAhead;
     uint32_t stage = units;
-    if constexpr (kAt == kStages) {
-      const uint32_t most = (l.x_lds / cnt - 16) / (kUnit * 2 + V::kSteps * 4);
-      if (most < units) stage = most / round * round;
-    }
+    if constexpr (kAt == kStages)
+      stage = stage_units(l.x_lds, cnt, V::kXUnit, l.k_waves * V::kUnits * V::kAhead, units);
     const uint32_t stride = kOwn ? kXRow : stage * (kUnit * 2) + 16, s_stride = stage * V::kSteps;
     float* const scales = reinterpret_cast<float*>(x_lds + cnt * stride);
     const uint8_t* const xa = (kOwn ? mine + V::kXAt : x_lds) +
@@ -772,12 +771,13 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
   while (l.k_waves < V::kWaves && l.k_waves * 4 <= units && work * l.k_waves < kCus * 6)
     l.k_waves *= 2;
   if constexpr (kAt == kStages) {
-    // a stage holds one round of the rings at least: 16 rows of one wave's two
-    // units, with 8 scales each, take 17 KB
-    constexpr uint32_t kTurnBytes = V::kUnits * (kUnit * 2 + V::kSteps * 4);
-    static_assert(kR * (V::kAhead * kTurnBytes + 16) <= kStageBytes, "a wave's round");
-    while (l.k_waves > 1 && l.pass * (l.k_waves * V::kAhead * kTurnBytes + 16) > l.x_lds)
-      l.k_waves /= 2;
+    // A stage holds one round of the rings at least (16 rows of one wave's two
+    // units, with 8 scales each, take 17 KB). One of no units would never end.
+    constexpr uint32_t kOfWave = V::kUnits * V::kAhead;
+    static_assert(stage_units(kStageBytes, kR, V::kXUnit, kOfWave, ~0u) > 0, "a wave's round");
+    l.k_waves = stage_waves(l.x_lds, l.pass, V::kXUnit, kOfWave, l.k_waves);
+    if (units && stage_units(l.x_lds, l.pass, V::kXUnit, l.k_waves * kOfWave, units) == 0)
+      return hipErrorInvalidValue;
   }
   // Workgroups of up to 8 waves (16 if alone), and how many column tiles a wave
   // takes one after the other with x where it is: the least time of the compute

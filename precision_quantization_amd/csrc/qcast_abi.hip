@@ -912,6 +912,7 @@ int qcast_combine_backward_per_token(const void* dout, const void* y, int64_t to
     return rc;
   if (tokens == 0 || top_k == 0) return QCAST_OK;
   if (cols == 0) return dw ? QCAST_ERR_SHAPE : QCAST_OK;      // dw over no columns
+  if (rows == 0 && !dw) return QCAST_OK;                      // q, sf and dy hold nothing
   if (!dout || !dest || (q != nullptr) != (sf != nullptr) || (!q && !dy && !dw) ||
       (dw && !y && rows > 0))
     return QCAST_ERR_NULL;

@@ -3,7 +3,7 @@ call."""
 import pytest
 
 from conftest import gpu_available
-from test_abi_moe import ERR_DEVICE, ERR_SHAPE, codes, lib  # noqa: F401
+from test_abi_moe import ERR_DEVICE, ERR_NULL, ERR_SHAPE, OK, bwd, codes, lib  # noqa: F401
 
 ROW, COL = 0, 2
 
@@ -30,3 +30,13 @@ def test_column_major_scales_of_one_long_row(lib):  # noqa: F811
     if not gpu_available():
         assert cast((1 << 36) - 64, 64, COL) == cast(1 << 36, 64, ROW) == cast(1 << 36, 64, COL | 4) == ERR_DEVICE
         assert cast(128 * ((1 << 31) // 3), 128, COL, rows=3) == ERR_DEVICE
+
+
+def test_combine_backward_without_rows(lib):  # noqa: F811
+    """Buffers of no rows have no address; only dw is written then."""
+    empty = dict(rows=0, q=None, sf=None, dy=None)
+    assert bwd(lib, **empty, dw=None) == bwd(lib, **empty, dw=None, y=None) == OK
+    assert bwd(lib, **empty, dw=None, cols=200) == bwd(lib, **empty, dw=None, top_k=65) == ERR_SHAPE
+    assert bwd(lib, **empty, dest=None) == ERR_NULL
+    if not gpu_available():
+        assert bwd(lib, **empty) == bwd(lib, **empty, y=None) == ERR_DEVICE

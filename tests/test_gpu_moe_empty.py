@@ -1,0 +1,47 @@
+"""Plans without rows (no expert of this rank was chosen, and the buffers are as
+short as that), in the same manner by every reader of a plan."""
+import pytest
+import torch
+
+import precision_quantization_amd as pq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def test_a_plan_without_rows():
+    tokens, top_k, cols, experts = 5, 3, 256, 4
+
+    def i32(*shape, fill=0):
+        return torch.full(shape, fill, dtype=torch.int32, device=DEV)
+    plan = pq.ExpertPlan(i32(tokens, top_k, fill=-1), i32(0), i32(experts + 1), i32(experts), None, 16)
+    x = torch.randn(tokens, cols, device=DEV).to(torch.bfloat16)
+    y = x[:0]
+    w = torch.rand(tokens, top_k, device=DEV)
+    q, sf = pq.qcast_dispatch_per_token(x, plan, w)
+    assert tuple(q.shape) == (0, cols) and tuple(sf.shape) == (0, 2)
+    moved, _ = pq.qcast_dispatch_codes(x, plan)
+    assert tuple(moved.shape) == (0, cols)
+    assert torch.equal(pq.qcast_combine(y, plan.dest, w, x), x)
+    assert not pq.qcast_combine(y, plan.dest, w).any()
+    back = pq.qcast_combine_backward_per_token(x, plan, None, w, want_dy=True)
+    assert tuple(back.out.shape) == tuple(back.dy.shape) == (0, cols) and back.dw is None
+    back = pq.qcast_combine_backward_per_token(x, plan, y, w)
+    assert tuple(back.dw.shape) == (tokens, top_k) and not back.dw.any()
+    back = pq.qcast_combine_backward_per_token(x, plan, y, w, want_codes=False)
+    assert not back.dw.any()
+
+
+def test_no_expert_here():
+    """The same from the sort: rows for slots that all go elsewhere."""
+    ids = torch.full((5, 3), 9, device=DEV)
+    plan = pq.qcast_expert_sort(ids, 4, 16)
+    assert (plan.dest == -1).all() and (plan.source == -1).all() and not plan.offsets.any() and not plan.counts.any()
+    x = torch.randn(5, 256, device=DEV).to(torch.bfloat16)
+    rows = plan.source.shape[0]
+    y = torch.full((rows, 256), float("nan"), dtype=torch.bfloat16, device=DEV)
+    out = torch.full((rows, 256), 7, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    back = pq.qcast_combine_backward_per_token(x, plan, y, out=out)
+    assert not back.dw.any() and (out.view(torch.uint8) == 7).all()
+    pq.qcast_dispatch_per_token(x, plan, out=out)
+    assert (out.view(torch.uint8) == 7).all() and torch.equal(pq.qcast_combine(y, plan.dest, None, x), x)

@@ -895,6 +895,8 @@ def qcast_norm_backward_per_token(dx, saved_h, rstd_pre, w_pre, dh=None, saved_h
 
 # ---- a mixture-of-experts layer around its products -------------------------
 
+MAX_EXPERTS = 1024              # QCAST_MAX_EXPERTS
+MAX_ALIGN = 1024                # QCAST_MAX_ALIGN
 ExpertPlan = namedtuple("ExpertPlan", "dest source offsets counts row_weight align")
 CombineGrad = namedtuple("CombineGrad", "out out_sf dy dw")
 
@@ -935,19 +937,23 @@ def qcast_expert_sort(ids, experts, align=1, first=0, weight=None, stream=None):
     ptr, width = _ids(ids, "ids", 2)
     tokens, top_k = ids.shape
     experts, align = int(experts), int(align)
+    if not 1 <= experts <= MAX_EXPERTS:
+        raise QcastError(2, f"experts must be 1 to {MAX_EXPERTS}, got {experts}")
+    if not 1 <= align <= MAX_ALIGN:
+        raise QcastError(8, f"align must be a power of two up to {MAX_ALIGN}, got {align}")
     dev = ids.device
     wptr = None if weight is None else _like(weight, (tokens, top_k), torch.float32, dev, "weight")
-    rows = expert_rows(tokens, top_k, experts, align) if align > 0 and experts > 0 else 0
+    rows = expert_rows(tokens, top_k, experts, align)
     parts = _sort_parts(tokens * top_k)
     i32 = torch.int32
     sh, ctx = _placed(dev, stream)
     with ctx:
         dest = _new((tokens, top_k), i32)
         source = _new((rows,), i32)
-        offsets = _new((max(experts, 0) + 1,), i32)
-        counts = _new((max(experts, 0),), i32)
+        offsets = _new((experts + 1,), i32)
+        counts = _new((experts,), i32)
         row_weight = None if wptr is None else _new((rows,), torch.float32)
-        ws = _new((parts * experts,), i32) if parts and experts > 0 else None
+        ws = _new((parts * experts,), i32) if parts else None
         check(load().qcast_expert_sort(ptr, width, tokens, top_k, experts, first, align, wptr,
                                        dest.data_ptr(), source.data_ptr(), offsets.data_ptr(),
                                        counts.data_ptr(), _ptr(row_weight), _ptr(ws), sh),

@@ -603,12 +603,14 @@ QCAST_API int qcast_norm_backward_per_token(
  * experts; its slot k is the pair (token, k), slot number token * top_k + k.
  * qcast_expert_sort gives every slot a row, the rows of one expert together;
  * qcast_dispatch_* bring the tokens' rows there, qcast_combine brings the
- * products' rows back, and qcast_combine_backward_per_token is its gradient
- * (the gradient of a dispatch is the unweighted qcast_combine). For a few
- * tokens qcast_matvec_e2m1 takes each slot's expert by itself: nothing is
- * sorted. Shared limits: top_k <= QCAST_MAX_TOP_K, experts <=
- * QCAST_MAX_EXPERTS, align a power of two <= QCAST_MAX_ALIGN, slots and rows
- * < 2^31.
+ * products' rows back, and qcast_combine_backward_per_token is its gradient.
+ * The gradient of a dispatch is the qcast_combine of the rows' gradient with
+ * the dispatch's weights (NULL: none), and that of its weights is the dw of
+ * qcast_combine_backward_per_token with the dispatched x as dout and the rows'
+ * gradient as y. For a few tokens qcast_matvec_e2m1 takes each slot's expert by
+ * itself: nothing is sorted. Shared limits: top_k <= QCAST_MAX_TOP_K, experts
+ * <= QCAST_MAX_EXPERTS, align a power of two <= QCAST_MAX_ALIGN, slots and
+ * rows < 2^31.
  */
 #define QCAST_MAX_EXPERTS 1024
 #define QCAST_MAX_TOP_K 64

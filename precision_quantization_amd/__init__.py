@@ -1045,7 +1045,8 @@ def qcast_combine(y, dest=None, weight=None, base=None, top_k=None, out=None, st
     top_k]``: int32 (an ``ExpertPlan``'s), -1 where there is no row; None:
     ``y`` holds a token's ``top_k`` rows next to one another. ``weight
     [tokens, top_k]`` fp32 (None: ones); ``base [tokens, cols]`` bf16 (None:
-    zeros). Without weight and base it is the gradient of a dispatch."""
+    zeros). Without base, of the rows' gradient and with the weights that a
+    dispatch had, it is that dispatch's gradient."""
     y = _bf16_input(y, "y")
     rows, cols = y.shape
     dev = y.device
@@ -1078,7 +1079,8 @@ def qcast_combine_backward_per_token(dout, plan, y=None, weight=None, fmt="e4m3"
     gradient: a ``CombineGrad`` of ``out [rows, cols]``/``out_sf`` (with
     ``want_codes``), the same in bf16 ``dy`` (with ``want_dy``) and, where
     ``y`` (the forward's) is given, ``dw [tokens, top_k]`` fp32, the gradient
-    of ``weight``. Padding rows and rows behind the last run as
+    of ``weight`` (of a dispatch's weights: with its ``x`` as ``dout`` and its
+    rows' gradient as ``y``). Padding rows and rows behind the last run as
     qcast_dispatch_per_token leaves them."""
     f = fmt_id(fmt)
     dout = _bf16_input(dout, "dout")

@@ -45,3 +45,26 @@ def test_no_expert_here():
     assert not back.dw.any() and (out.view(torch.uint8) == 7).all()
     pq.qcast_dispatch_per_token(x, plan, out=out)
     assert (out.view(torch.uint8) == 7).all() and torch.equal(pq.qcast_combine(y, plan.dest, None, x), x)
+
+
+@pytest.mark.parametrize("tokens", [5, 20000])
+def test_tokens_without_slots(tokens):
+    """top_k 0: the base alone, or zeros."""
+    x = torch.randn(tokens, 264, device=DEV).to(torch.bfloat16)
+    dest = torch.zeros(tokens, 0, dtype=torch.int32, device=DEV)
+    assert torch.equal(pq.qcast_combine(x[:3], dest, None, x), x)
+    out = torch.full((tokens, 264), 7.0, dtype=torch.bfloat16, device=DEV)
+    assert not pq.qcast_combine(x[:3], dest, out=out).any()
+    plan = pq.qcast_expert_sort(torch.zeros(tokens, 0, dtype=torch.int64, device=DEV), 4, 16)
+    assert tuple(plan.dest.shape) == (tokens, 0) and plan.source.shape[0] == 0
+    assert not plan.offsets.any() and not plan.counts.any()
+
+
+@pytest.mark.parametrize("experts,k", [(0, 256), (3, 0), (0, 0)])
+def test_products_with_no_expert_or_no_k(experts, k):
+    x = torch.ones(4, k, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(experts, 40, k // 2, dtype=torch.uint8, device=DEV)
+    sf = torch.ones(experts, 40, k // 32, device=DEV)
+    ids = torch.arange(8, device=DEV) % 4
+    out = torch.full((8, 40), 7.0, device=DEV)
+    assert not pq.qcast_matvec_e2m1(x, w, sf, ids, out_dtype=torch.float32, out=out).any()

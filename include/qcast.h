@@ -760,8 +760,11 @@ QCAST_API int qcast_combine_backward_per_token(
  *   Products of w's codes with x (bf16, or its codes) are summed over up to 128 k
  *   ahead of the scales, w_sf is applied ahead of x_sf or as w_sf * x_sf: these
  *   sums and products have to stay within fp32's range.
- *   Made for up to some 16 rows an expert: more are taken 16 at a time, each
- *   time reading the weights again.
+ *   Made for up to some 16 rows an expert. An expert's rows are taken so many at
+ *   a time, each time reading its weights again: up to 16 without ids or with
+ *   more rows than experts; up to 4 with ids and as many experts as rows or
+ *   more; one where those rows have a single row of x (a token's experts, which
+ *   are different ones).
  *   Limits: rows, n, experts < 2^31, k < 2^24, rows * n < 2^40, and fewer than 2^31
  *   tiles of 16 columns of the rows' (or, where there are fewer, the) experts.
  */
@@ -787,7 +790,8 @@ QCAST_API int qcast_abi_version(void);
  * count_ws NULL) and that of qcast_norm_per_token, whose workgroups walk the
  * rows. qcast_norm_backward_per_token walks them too, but its grid, which
  * fixes the order of its sums, follows from the sizes alone
- * (qcast_norm_ws_rows); every other launch takes one workgroup per unit of
+ * (qcast_norm_ws_rows); that of qcast_matvec_e2m1 from the sizes and the 256
+ * units of a whole card; every other launch takes one workgroup per unit of
  * work. These ignore it.
  */
 QCAST_API void qcast_set_num_cus(int n);

@@ -19,7 +19,7 @@ __device__ __forceinline__ uint32_t scale_index(uint32_t row, uint32_t w, uint32
   return pad ? w * pad + row : row * words + w;
 }
 
-// Pieces of a token: kSeg of 64 chunks each, then one for its scales.
+// Pieces of a token: one for each 64 chunks, then one for its scales.
 __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes p, uint32_t pieces,
                                                                   uint32_t groups,
                                                                   uint32_t first) {
@@ -67,7 +67,10 @@ __global__ __launch_bounds__(kThreads) void dispatch_codes_kernel(DispatchCodes 
   }
 }
 
-// Without weights a row is cast once, whatever the number of its places.
+// Without weights a row is cast once, whatever the number of its places (4096 x 8
+// of 7168, runs of 128: 54 us). With weights each place is: its weight is loaded
+// behind the stores of the place before, and its groups' maxima are formed again
+// (65 to 84 us).
 template <int kFmt, bool kWeighted>
 __global__ __launch_bounds__(kThreads) void dispatch_cast_kernel(DispatchCast p, uint32_t segs,
                                                                  uint32_t groups, uint32_t first) {

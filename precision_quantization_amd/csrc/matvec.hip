@@ -3,8 +3,8 @@
 // out[r][i] = sum_g sf[i][g] * (sum_{j in g} code[i][j] * x[r][j]), the inner
 // sum over one scale group in the matrix cores (an E2M1 value and an 8-bit
 // code are bf16 values: nothing is rounded on the way in), the outer one in
-// fp32. A weight is read once for up to 16 rows that share it: bound by HBM
-// reads of the weights.
+// fp32. A weight is read once for the rows of a pass that share it (up to 16,
+// launch_matvec): bound by HBM reads of the weights.
 //
 // gfx950 design. v_mfma_f32_16x16x32_bf16 with x as A (16 rows) and the
 // weights as B (16 columns, which are 16 rows of w): of one step's 32 k, lane
@@ -23,9 +23,11 @@
 // tile take its turns in turn and add their sums in a fixed order. x is in LDS
 // for the whole workgroup: all of it, or stages of it. Many rows without experts
 // bring theirs with the weights instead, through the wave's own LDS, so that no
-// wave waits for another. One row of 7168 x 18432 in groups of 32: 18.2 us (82.6
-// MB, 4.5 TB/s); 8 experts' 4096 x 7168 in groups of 128: 25.5 us (4.9 TB/s); 16
-// tokens to 8 of 32 experts of 7168 x 2048, groups of 32: 60 us (4.1 TB/s).
+// wave waits for another. One row of 7168 x 18432 in groups of 32: 19 us (82.6
+// MB, 4.3 TB/s); 8 experts' 4096 x 7168 in groups of 128: 26 us (4.8 TB/s); 16
+// tokens to 8 of 32 experts of 7168 x 2048, groups of 32: 54 to 60 us (28 experts
+// hit, 217 MB, 3.6 to 4.0 TB/s). Every variant spills 43 to 84 scalar registers, a
+// third of them, all with 8-bit x, up to 22 vector registers a lane.
 #include "qcast_device.h"
 #include "qcast_kernels.h"
 #include "qcast_row.h"
@@ -724,6 +726,8 @@ __global__ __launch_bounds__((kAt == kWithW ? 512 : 1024)) void matvec_kernel(Ma
   }
 }
 
+// The launch shapes, and with them the order of the sums, are those of a whole
+// card, whatever the partition or qcast_set_num_cus.
 constexpr uint32_t kCus = 256;
 
 // LDS for the whole of x at most, and for a stage of it; with few tiles, for
@@ -820,8 +824,9 @@ hipError_t launch_variant(MatvecLaunch l, hipStream_t stream) {
   });
 }
 
-// Where x is. Whole up to 72 KB (5 rows of 16384 x 5120: 14.7 us, 18.7 with the
-// weights; 16 tokens to 8 of 32 experts of 7168 x 2048: 60, 68 in stages). Past
+// Where x is. Whole up to 72 KB (5 rows of 16384 x 5120: 14 us, 19 with the
+// weights; 16 tokens to 8 of 32 experts of 7168 x 2048: 54 to 60, 82 to 90 in
+// stages). Past
 // that the rows of an expert come in stages (8 tokens to 8 of 32 experts of
 // 4096 x 7168: 80 us, 109 with the weights), and so do up to four rows without
 // experts; more of those, whose workgroups would each stage all of x for few

@@ -30,8 +30,8 @@ __device__ __forceinline__ void pad_range(const ExpertRuns& r, uint32_t g, uint3
   last = end - from < kPadRows ? (uint32_t)end : first + kPadRows;
 }
 
-// The rows of a token's slots k0 .. k0 + 7, the same in every lane; past_rows
-// (no row) behind its last slot. One batch of scalar loads.
+// The rows of a token's slots k0 .. k0 + 7, the same in every lane; kNoRow behind
+// its last slot. One batch of loads, vector loads where the kernel's loop stores.
 constexpr int kBatch = 8;
 constexpr uint32_t kNoRow = 0xffffffffu;
 __device__ __forceinline__ void slot_rows(const int32_t* dest, uint32_t k0, uint32_t top_k,

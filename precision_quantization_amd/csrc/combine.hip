@@ -73,10 +73,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(Combine p, uint32_t s
 // A wave takes one slot over all columns, 512 at a time, with the next 512 asked
 // for ahead (the loop's end waits for them and, as the number of stores is not
 // known there, for this step's stores); the waves of a token's slots read its dout
-// from the caches. What is not asked for is a buffer of no bytes. 4096 x 8 x 7168 with codes and dw: 150
-// us (800 MB with the padding, 5.3 TB/s), as with two or four slots a wave (150
-// and 153), or a wave for 512 columns of all slots with a join of dw's parts
-// (151); 257 x 6 x 2048: 6.0, 6.4, 8.7 and 9.2.
+// from the caches. What is not asked for is a buffer of no bytes. 4096 x 8 x 7168
+// with codes and dw: 150 us (800 MB with the padding, 5.3 TB/s), as with two or
+// four slots a wave (150 and 153), or a wave for 512 columns of all slots with a
+// join of dw's parts (151); 257 x 6 x 2048: 6.0, 6.4, 8.7 and 9.2.
 template <int kFmt>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(DispatchCast p,
                                                                     uint32_t groups,
@@ -147,8 +147,8 @@ hipError_t launch_combine(const Combine& p, hipStream_t stream) {
   const uint32_t segs = (p.chunks + 63) / 64;
   // Four tokens of one or two slots where there is more than the card holds at
   // once, 8192 waves, twice over (16384 x 1 x 2048: 41 to 44 us with one token a
-  // wave, 32 to 34 with four; 8399 x 2 x 1408, a quarter of the slots with rows: 17.6 and 13.1;
-  // two tokens of four slots, 8192 x 4 x 2048: 33.4 and 33.8).
+  // wave, 32 to 34 with four; 8399 x 2 x 1408, a quarter of the slots with rows:
+  // 17.6 and 13.1; two tokens of four slots, 8192 x 4 x 2048: 33.4 and 33.8).
   const bool four = p.top_k <= 2 && (uint64_t)p.tokens * segs >= 2 * 8192;
   const uint32_t tokens = four ? 4 : 1;
   const uint64_t items = ((uint64_t)p.tokens + tokens - 1) / tokens * segs;
